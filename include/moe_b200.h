@@ -249,6 +249,78 @@ MOE_API int moe_forward_noalloc(int T, int d_model, int d_ff, int n_experts, int
                                 const uint8_t *w2_codes, const uint8_t *w2_scales, const uint16_t *b2,
                                 const uint16_t *norm_scale, uint16_t *y, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Dense 8-bit operators: the products a layer takes beside its routed experts
+ * (a dense or shared feed-forward block, the projections around it, logits).
+ * (The gpt-oss write-ups have no counterpart; the norm and the clamped gated
+ * activation are the block's.)
+ *
+ * An 8-bit matrix is E4M3 codes and fp32 scales; an element's value is its code
+ * times its block's scale:
+ *   activations  u8 [M, K] and fp32 [M, ceil(K/128)]: a scale for each 128
+ *                consecutive elements of a row
+ *   weights      u8 [N, K] and fp32 [ceil(N/128), ceil(K/128)]: a scale for each
+ *                128 x 128 block (blocks at the right and lower edges are smaller)
+ * E4M3 outputs take the scale s = max(max|v| / 448, 2^-126) of their block and
+ * round v / s to nearest even.  Products and sums are fp32; an output is rounded
+ * once.  A NaN in a block makes its scale and all its codes NaN.
+ *
+ * No call allocates or keeps anything: there is no workspace, and calls on one
+ * context may overlap (streams, host threads, captured graphs).  Results do not
+ * depend on timing: the same inputs give the same bits.  Outputs must not
+ * overlap inputs except where stated.  The context's device is made current
+ * during a call; pointers and stream belong to it. */
+
+enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 };   /* types of x, residual, sum and c */
+
+typedef struct moe_fp8_ctx moe_fp8_ctx_t;
+
+/* Create a context on the current device: its SM count and the latched error
+ * word of the bounded waits.  Call it outside stream captures. */
+MOE_API int moe_fp8_init(moe_fp8_ctx_t **out);
+MOE_API int moe_fp8_destroy(moe_fp8_ctx_t *ctx);
+
+/* As moe_sync_status and moe_set_wait_limit_ns. */
+MOE_API int moe_fp8_sync_status(moe_fp8_ctx_t *ctx, void *stream);
+MOE_API int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *ctx, unsigned long long ns);
+
+/* n = x + residual (residual may be NULL: n = x), in fp32;
+ * sum_out = n rounded to `type` (may be NULL; may be x or residual themselves,
+ * with the same row distance);
+ * q, q_scale = n / sqrt(mean(n^2) + eps) * norm_scale in E4M3.
+ * x, residual, sum_out: type [T, d], rows ldx / ldr / lds elements apart (whole
+ * 16-byte units); norm_scale bf16 [d]; q u8 [T, d]; q_scale fp32 [T, ceil(d/128)].
+ * d: multiple of 16, 16..16384. */
+MOE_API int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *ctx, int T, int d, int type, const void *x, int64_t ldx,
+                        const void *residual, int64_t ldr, const uint16_t *norm_scale, float eps, void *sum_out,
+                        int64_t lds, uint8_t *q, float *q_scale, void *stream);
+
+/* c[m, n] = sum_k a[m, k] b[n, k] (+ bias[n]) (+ residual[m, n]), rounded once to `type`.
+ * a u8 [M, K], rows lda bytes apart (multiple of 16); b u8 [N, K]; K a multiple of 16;
+ * bias bf16 [N] or NULL; c, residual: type [M, N], rows ldc / ldr elements apart;
+ * residual may be NULL, or c itself.  a and b 16-byte aligned, c and residual to their
+ * type (rows on 16-byte units are the fast case). */
+MOE_API int moe_fp8_matmul(moe_fp8_ctx_t *ctx, int M, int N, int K, const uint8_t *a, int64_t lda,
+                   const float *a_scale, const uint8_t *b, const float *b_scale, const uint16_t *bias,
+                   const void *residual, int64_t ldr, void *c, int64_t ldc, int type, void *stream);
+
+/* The first half of a gated feed-forward block in one launch:
+ *   g = min(W13_gate a + b_gate, limit),  u = clamp(W13_linear a + b_linear, -limit, limit),
+ *   h = g * sigmoid(alpha g) * (u + shift), then E4M3 with a scale per 128 columns.
+ * (alpha, limit, shift) = (1.702, 7, 1) is the experts' activation, (1, INFINITY, 0) is
+ * silu(gate) * linear.  a, a_scale as above; w13 u8 [2, F, K] (gate rows, then linear rows),
+ * w13_scale fp32 [2, ceil(F/128), ceil(K/128)] (each half has its own blocks), b13 bf16
+ * [2, F] or NULL; h u8 [M, F], h_scale fp32 [M, ceil(F/128)].  F a multiple of 16. */
+MOE_API int moe_fp8_gated_matmul(moe_fp8_ctx_t *ctx, int M, int F, int K, const uint8_t *a, int64_t lda,
+                         const float *a_scale, const uint8_t *w13, const float *w13_scale, const uint16_t *b13,
+                         float alpha, float limit, float shift, uint8_t *h, float *h_scale, void *stream);
+
+/* The launch plan of moe_fp8_matmul (gated 0) or moe_fp8_gated_matmul (gated 1, N = F),
+ * computed on the host alone.  Writes out[0..11] = {accumulator columns per CTA, CTAs per MMA,
+ * CTAs sharing a gated block, rows of an A stage, stages, row tiles, tiles, grid, shared
+ * memory taken, shared memory needed, TMEM columns, CTAs per SM}.  For tests of the planner. */
+MOE_API int moe_fp8_debug_plan(int gated, int M, int N, int K, int num_sms, int *out);
+
 /* A human-readable name of an error code. */
 MOE_API const char *moe_strerror(int code);
 

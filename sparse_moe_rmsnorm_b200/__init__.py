@@ -24,6 +24,9 @@ __all__ = [
     "moe_expert_ffn", "moe_finalize", "moe_copy_workspace", "moe_sync_status", "moe_set_wait_limit_ns",
     "moe_selftest_wait_timeout", "moe_debug_decode", "moe_debug_plan", "moe_strerror", "moe_version", "WS",
     "moe_forward_noalloc", "MOE_NOALLOC_MAX_TOKENS",
+    "MOE_BF16", "MOE_FP16", "MOE_FP32", "Fp8Ops", "DenseFFN", "DenseWeights", "quantize_fp8_rows", "quantize_fp8_weight",
+    "moe_fp8_init", "moe_fp8_destroy", "moe_fp8_sync_status", "moe_fp8_set_wait_limit_ns", "moe_add_rmsnorm_fp8",
+    "moe_fp8_matmul", "moe_fp8_gated_matmul", "moe_fp8_debug_plan",
 ]
 
 MOE_NOALLOC_MAX_TOKENS = 64
@@ -74,6 +77,19 @@ _SIGS = {
                                         ctypes.c_void_p, ctypes.c_void_p]),
     "moe_forward_noalloc": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_float] + [ctypes.c_void_p] * 12),
     "moe_debug_plan": (ctypes.c_int, [ctypes.c_int] * 8 + [ctypes.c_void_p]),
+    "moe_fp8_init": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p)]),
+    "moe_fp8_destroy": (ctypes.c_int, [ctypes.c_void_p]),
+    "moe_fp8_sync_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "moe_fp8_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_ulonglong]),
+    "moe_add_rmsnorm_fp8": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 3
+                            + [ctypes.c_void_p, ctypes.c_int64] * 2 + [ctypes.c_void_p, ctypes.c_float]
+                            + [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 3),
+    "moe_fp8_matmul": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int64]
+                       + [ctypes.c_void_p] * 4 + [ctypes.c_void_p, ctypes.c_int64] * 2
+                       + [ctypes.c_int, ctypes.c_void_p]),
+    "moe_fp8_gated_matmul": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int64]
+                             + [ctypes.c_void_p] * 4 + [ctypes.c_float] * 3 + [ctypes.c_void_p] * 3),
+    "moe_fp8_debug_plan": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p]),
     "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_version": (ctypes.c_char_p, []),
 }
@@ -361,3 +377,10 @@ class MoE:
 
     def sync_status(self, stream=None) -> int:
         return moe_sync_status(self.ctx, stream)
+
+
+from .fp8 import (  # noqa: E402  (it calls this module's helpers)
+    MOE_BF16, MOE_FP16, MOE_FP32, DenseFFN, DenseWeights, Fp8Ops, moe_add_rmsnorm_fp8, moe_fp8_debug_plan,
+    moe_fp8_destroy, moe_fp8_gated_matmul, moe_fp8_init, moe_fp8_matmul, moe_fp8_set_wait_limit_ns,
+    moe_fp8_sync_status, quantize_fp8_rows, quantize_fp8_weight,
+)

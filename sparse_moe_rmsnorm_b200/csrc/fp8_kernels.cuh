@@ -1,0 +1,128 @@
+// Parameter blocks and host-side launch plan of the dense 8-bit operators.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace moe {
+
+constexpr int FP8_BLOCK = 128;                 // elements (of a row, or rows and columns of a weight) per scale
+constexpr float FP8_MAX = 448.0f;              // largest E4M3 value
+constexpr float FP8_SCALE_MIN = 1.17549435e-38f;   // 2^-126: the scale of a block of zeros
+
+enum { FP8_BF16 = 0, FP8_FP16 = 1, FP8_FP32 = 2 };   // MOE_BF16, MOE_FP16, MOE_FP32 of the C ABI
+
+__host__ __device__ inline int fp8_blocks(int n) { return (n + FP8_BLOCK - 1) / FP8_BLOCK; }
+
+struct Fp8NormParams {
+    const void *x, *residual;       // [T, d], rows ldx / ldr elements apart; residual may be NULL
+    const uint16_t *norm_scale;     // bf16 [d]
+    void *sum_out;                  // [T, d], rows lds elements apart, or NULL
+    uint8_t *q;                     // E4M3 [T, d]
+    float *q_scale;                 // [T, ceil(d / 128)]
+    long long ldx, ldr, lds;
+    int T, d;
+    float eps;
+};
+
+struct Fp8GemmParams {
+    CUtensorMap map_a;              // u8 {K, M, 1}, box {128, a_rows, 1}
+    CUtensorMap map_b;              // u8 {K, N, 1}, box {128, BN / CTAS, 1}; gated {K, F, 2}, box {128, half, 1}
+    const float *a_scale;           // [M, KB]
+    const float *b_scale;           // [NB, KB]; gated [2, NB, KB]
+    int M, N, K, KB, NB;            // N: output columns (gated: F)
+    int m_tiles, tiles;
+    int a_rows, n_stages;           // rows of an A stage (128, or M rounded up to 8 below that)
+    const uint16_t *bias;           // bf16 [N] (gated [2 F]) or NULL
+    const void *residual;           // type [M, N], rows ldr elements apart, or NULL
+    void *c;                        // type [M, N], rows ldc elements apart
+    long long ldr, ldc;
+    int type;                       // FP8_BF16, FP8_FP16 or FP8_FP32
+    int vec_c, vec_r;               // rows of c / of the residual start on 16 bytes
+    float alpha, limit, shift;      // gated activation
+    uint8_t *h;                     // gated: E4M3 [M, F]
+    float *h_scale;                 // gated: [M, NB]
+    unsigned int *err;
+    unsigned long long wait_limit_ns;
+};
+
+// One kernel variant: BN columns of accumulators per CTA (gated: BN / 2 gate and BN / 2 linear
+// columns), CTAS CTAs per MMA, CL CTAs of a cluster sharing a gated row's 128-column block.
+struct Fp8Plan {
+    int bn, ctas, cl;
+    int a_rows, n_stages;
+    int m_tiles, tiles, grid, smem, tmem_cols;
+};
+
+constexpr int FP8_BM = 128;             // rows of A per CTA (TMEM lanes)
+constexpr int FP8_KS = 128;             // K elements per stage: one scale block
+constexpr int FP8_STAGES_MAX = 16;
+constexpr int FP8_SMEM_SM = 227 * 1024; // shared memory of a CTA that has its SM alone
+// ... and of one of two CTAs on an SM: an SM's 228 KB hold two of these and the 1 KB that each reserves.
+constexpr int FP8_SMEM_HALF = 113 * 1024;
+
+__host__ __device__ constexpr int fp8_wgs(int bn) { return bn >= 128 ? 2 : 1; }      // epilogue warpgroups
+__host__ __device__ constexpr int fp8_bufs(int bn) { return bn == 256 ? 2 : bn == 32 ? 8 : 4; }   // accumulators
+// A variant takes its share of an SM's shared memory as it takes TMEM (512 or 256 of the 512
+// columns), whatever its rings need: CTAs that fit an SM together then find their TMEM columns
+// free, so no allocation waits while a CTA of the same cluster waits for it.
+__host__ __device__ constexpr int fp8_ctas_per_sm(int bn) { return fp8_bufs(bn) * bn == 512 ? 1 : 2; }
+__host__ __device__ constexpr int fp8_smem_bytes(int bn) { return fp8_ctas_per_sm(bn) == 1 ? FP8_SMEM_SM : FP8_SMEM_HALF; }
+__host__ __device__ constexpr int fp8_threads(int bn) { return fp8_wgs(bn) * 128 + 64; }
+
+// Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's 4 KB staging
+// tile, the barriers, the row maxima that warps or CTAs exchange, the TMEM base and abort flag.
+struct Fp8Smem {
+    int a_stage, b_stage, b_off, stage_off, bar_off, ex_off, misc_off, total;
+};
+
+__host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int cl, int gated, int a_rows, int n_stages) {
+    Fp8Smem s;
+    s.a_stage = a_rows * FP8_KS;
+    s.b_stage = bn / ctas * FP8_KS;
+    s.b_off = n_stages * s.a_stage;
+    s.stage_off = s.b_off + n_stages * s.b_stage;
+    s.bar_off = s.stage_off + (gated ? 0 : fp8_wgs(bn) * 4 * 4096);
+    // full and empty per stage, full and empty per accumulator, drain, exchange [4 quarters][2 parities]
+    s.ex_off = s.bar_off + (2 * n_stages + 2 * fp8_bufs(bn) + 1 + 8) * 8;
+    s.ex_off = (s.ex_off + 15) / 16 * 16;
+    s.misc_off = s.ex_off + (gated ? 2 * (fp8_wgs(bn) > cl ? fp8_wgs(bn) : cl) * FP8_BM * 4 : 0);
+    s.total = s.misc_off + 16;
+    // the MMA reads 128 rows of A from a stage's start, also where a stage holds fewer
+    const int a_end = (n_stages - 1) * s.a_stage + FP8_BM * FP8_KS;
+    if (s.total < a_end) s.total = a_end;
+    s.total += 1024;
+    return s;
+}
+
+// The variant, ring depth and grid of one product.  Returns false when the sizes are out of range.
+inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, Fp8Plan *pl) {
+    const long long rows = (M + FP8_BM - 1) / FP8_BM;
+    auto cols = [&](int bn) -> long long { return gated ? fp8_blocks(N) : (N + bn - 1) / bn; };
+    pl->ctas = 1;
+    if (gated) {
+        pl->bn = rows * cols(64) * 4 >= num_sms ? 64 : 32;
+        pl->cl = FP8_BLOCK / (pl->bn / 2);
+    } else {
+        pl->bn = rows * cols(128) >= num_sms ? 128 : rows * cols(64) >= num_sms ? 64 : 32;
+        pl->cl = 1;
+    }
+    const long long tiles = rows * cols(pl->bn);
+    if (tiles > (1 << 30)) return false;
+    pl->m_tiles = (int)rows;
+    pl->tiles = (int)tiles;
+    pl->a_rows = M < FP8_BM ? (M + 7) / 8 * 8 : FP8_BM;
+    pl->tmem_cols = fp8_bufs(pl->bn) * pl->bn;
+    pl->smem = fp8_smem_bytes(pl->bn);
+    int ns = FP8_STAGES_MAX;
+    while (ns > 2 && fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) --ns;
+    if (fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) return false;
+    pl->n_stages = ns;
+    const int group = pl->ctas == 2 ? 2 : pl->cl;
+    const long long most = (long long)num_sms * fp8_ctas_per_sm(pl->bn) / group;     // clusters that fit at once
+    pl->grid = (int)(tiles < most ? tiles : most) * group;
+    return true;
+}
+
+}  // namespace moe

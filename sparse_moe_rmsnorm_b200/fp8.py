@@ -1,0 +1,366 @@
+"""Dense 8-bit operators beside the routed experts, and the dense feed-forward block built of them.
+
+A matrix in 8 bits is a pair of tensors: E4M3 codes (``torch.float8_e4m3fn``, or the same bytes as
+``torch.uint8``) and fp32 scales.  Activations ``[M, K]`` have a scale for each 128 consecutive elements
+of a row (``[M, ceil(K/128)]``), weights ``[N, K]`` one for each 128 x 128 block
+(``[ceil(N/128), ceil(K/128)]``).
+
+Like the rest of the package this only checks and marshals arguments: the work is in the CUDA
+library, every call raises where the library or a B200 is missing, and a call returns when its kernel
+is queued.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+import math
+from typing import Dict, Optional
+
+import sparse_moe_rmsnorm_b200 as _moe
+
+__all__ = [
+    "MOE_BF16", "MOE_FP16", "MOE_FP32", "Fp8Ops", "DenseFFN", "DenseWeights", "quantize_fp8_rows", "quantize_fp8_weight",
+    "moe_fp8_init", "moe_fp8_destroy", "moe_fp8_sync_status", "moe_fp8_set_wait_limit_ns", "moe_add_rmsnorm_fp8",
+    "moe_fp8_matmul", "moe_fp8_gated_matmul", "moe_fp8_debug_plan",
+]
+
+MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
+
+FP8_BLOCK = 128
+FP8_MAX = 448.0
+FP8_SCALE_MIN = 2.0 ** -126
+
+
+# ------------------------------------------------------- C-ABI-named wrappers
+
+def moe_fp8_init() -> int:
+    h = ctypes.c_void_p()
+    _moe._check(_moe.lib().moe_fp8_init(ctypes.byref(h)), "moe_fp8_init")
+    return h.value
+
+
+def moe_fp8_destroy(ctx: int) -> None:
+    _moe.lib().moe_fp8_destroy(ctx)
+
+
+def moe_fp8_sync_status(ctx, stream=None) -> int:
+    return int(_moe.lib().moe_fp8_sync_status(ctx, _moe._stream(stream)))
+
+
+def moe_fp8_set_wait_limit_ns(ctx, ns: int) -> None:
+    _moe._check(_moe.lib().moe_fp8_set_wait_limit_ns(ctx, int(ns)), "moe_fp8_set_wait_limit_ns")
+
+
+def moe_add_rmsnorm_fp8(ctx, T, d, type, x, ldx, residual, ldr, norm_scale, eps, sum_out, lds, q, q_scale,
+                        stream=None) -> None:
+    p = _moe._ptr
+    _moe._check(_moe.lib().moe_add_rmsnorm_fp8(ctx, T, d, type, p(x), ldx, p(residual), ldr, p(norm_scale), eps,
+                                               p(sum_out), lds, p(q), p(q_scale), _moe._stream(stream)),
+                "moe_add_rmsnorm_fp8")
+
+
+def moe_fp8_matmul(ctx, M, N, K, a, lda, a_scale, b, b_scale, bias, residual, ldr, c, ldc, type, stream=None) -> None:
+    p = _moe._ptr
+    _moe._check(_moe.lib().moe_fp8_matmul(ctx, M, N, K, p(a), lda, p(a_scale), p(b), p(b_scale), p(bias), p(residual),
+                                          ldr, p(c), ldc, type, _moe._stream(stream)), "moe_fp8_matmul")
+
+
+def moe_fp8_gated_matmul(ctx, M, F, K, a, lda, a_scale, w13, w13_scale, b13, alpha, limit, shift, h, h_scale,
+                         stream=None) -> None:
+    p = _moe._ptr
+    _moe._check(_moe.lib().moe_fp8_gated_matmul(ctx, M, F, K, p(a), lda, p(a_scale), p(w13), p(w13_scale), p(b13), alpha,
+                                                limit, shift, p(h), p(h_scale), _moe._stream(stream)),
+                "moe_fp8_gated_matmul")
+
+
+FP8_PLAN_FIELDS = ("bn", "ctas", "cluster", "a_rows", "n_stages", "m_tiles", "tiles", "grid", "smem", "smem_needed",
+                   "tmem_cols", "ctas_per_sm")
+
+
+def moe_fp8_debug_plan(gated: bool, M: int, N: int, K: int, num_sms: int) -> Dict[str, int]:
+    """The launch plan of one product, computed on the host (N = F for the gated one)."""
+    out = (ctypes.c_int * len(FP8_PLAN_FIELDS))()
+    _moe._check(_moe.lib().moe_fp8_debug_plan(int(gated), int(M), int(N), int(K), int(num_sms), out),
+                "moe_fp8_debug_plan")
+    return dict(zip(FP8_PLAN_FIELDS, list(out)))
+
+
+# ------------------------------------------------------------- torch layer
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _bad(what: str) -> None:
+    raise _moe.MoEError(_moe.MOE_ERR_ARG, what)
+
+
+def _overlap(a, b) -> bool:
+    """Whether the byte ranges of two tensors meet."""
+    def span(t):
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+    if a is None or b is None or not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _same_place(a, b) -> bool:
+    return b is not None and a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+
+
+class Fp8Ops:
+    """The operators on one device.  One object serves any number of streams and captured graphs at once;
+    make it (and every shape's first call is like any other) outside a capture."""
+
+    def __init__(self, device=None):
+        import torch
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            _bad("Fp8Ops: not a CUDA device")
+        self._index = torch.cuda.current_device() if dev.index is None else dev.index
+        self.device = torch.device("cuda", self._index)
+        with torch.cuda.device(self._index):
+            self.ctx = moe_fp8_init()
+        self._lib = _moe.lib()
+        self._torch = torch
+        self._code = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
+        self._e4m3 = torch.float8_e4m3fn
+
+    def close(self) -> None:
+        if getattr(self, "ctx", None):
+            moe_fp8_destroy(self.ctx)
+            self.ctx = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # -- argument checks ---------------------------------------------------
+
+    def _rows(self, t, name, dtypes, rows=None, cols=None):
+        """The row distance of a matrix of this device whose rows are contiguous."""
+        if t.dim() != 2 or t.dtype not in dtypes or t.get_device() != self._index:
+            _bad("%s: a matrix of %s on %s is wanted, got %s %s on %s"
+                 % (name, " or ".join(map(str, dtypes)), self.device, tuple(t.shape), t.dtype, t.device))
+        r, c = t.shape
+        if (rows is not None and r != rows) or (cols is not None and c != cols):
+            _bad("%s: %s x %s is wanted, got %d x %d" % (name, rows, cols, r, c))
+        if c > 1 and t.stride(1) != 1:
+            _bad("%s: the elements of a row have to be contiguous" % name)
+        return t.stride(0) if r > 1 else -(-c // 16) * 16     # one row has no distance to the next
+
+    def _whole(self, t, name, dtype, shape):
+        """A contiguous tensor of this device."""
+        if t.dtype != dtype or tuple(t.shape) != shape or t.get_device() != self._index or not t.is_contiguous():
+            _bad("%s: a contiguous %s %s on %s is wanted, got %s %s on %s"
+                 % (name, dtype, shape, self.device, tuple(t.shape), t.dtype, t.device))
+
+    def _codes_whole(self, t, name, shape):
+        self._whole(t, name, t.dtype if t.dtype in (self._e4m3, self._torch.uint8) else self._e4m3, shape)
+
+    def _on(self, stream):
+        """(raw stream, context in which outputs are allocated): they belong to the stream that fills them."""
+        torch = self._torch
+        if stream is None:
+            return torch.cuda.current_stream(self._index).cuda_stream, None
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        return stream.cuda_stream, torch.cuda.stream(stream)
+
+    def _empty(self, where, *spec):
+        torch = self._torch
+        if where is None:
+            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in spec]
+        with where:
+            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in spec]
+
+    # -- operators ---------------------------------------------------------
+
+    def add_rmsnorm(self, x, norm_scale, residual=None, eps: float = 1e-5, sum_out=None, stream=None):
+        """RMS norm of ``x + residual`` (of ``x`` without one) in 8 bits: ``(q, q_scale, sum)``, without a
+        residual ``(q, q_scale)``.
+
+        ``x``, ``residual``: bf16, fp16 or fp32 ``[T, d]``, rows at any distance of whole 16 bytes;
+        ``norm_scale``: bf16 ``[d]``.  ``sum`` is ``x + residual`` in their type, written to ``sum_out`` if
+        given, which may be ``x`` or ``residual``.
+        """
+        torch = self._torch
+        code = self._code.get(x.dtype)
+        if code is None:
+            _bad("add_rmsnorm: x is bf16, fp16 or fp32, got %s" % x.dtype)
+        ldx = self._rows(x, "x", (x.dtype,))
+        T, d = x.shape
+        self._whole(norm_scale, "norm_scale", torch.bfloat16, (d,))
+        ldr = lds = 0
+        if residual is not None:
+            ldr = self._rows(residual, "residual", (x.dtype,), T, d)
+        elif sum_out is not None:
+            _bad("add_rmsnorm: there is no sum without a residual")
+        raw, where = self._on(stream)
+        spec = [((T, d), self._e4m3), ((T, _blocks(d)), torch.float32)]
+        if residual is not None and sum_out is None:
+            spec.append(((T, d), x.dtype))
+        out = self._empty(where, *spec)
+        if sum_out is not None:
+            for t in (x, residual):
+                if _overlap(sum_out, t) and not _same_place(sum_out, t):
+                    _bad("add_rmsnorm: sum_out overlaps an input without being it")
+            if _overlap(sum_out, norm_scale):
+                _bad("add_rmsnorm: sum_out overlaps norm_scale")
+            out.append(sum_out)
+        if residual is not None:
+            lds = self._rows(out[2], "sum_out", (x.dtype,), T, d)
+        rc = self._lib.moe_add_rmsnorm_fp8(
+            self.ctx, T, d, code, x.data_ptr(), ldx, residual.data_ptr() if residual is not None else None, ldr,
+            norm_scale.data_ptr(), eps, out[2].data_ptr() if residual is not None else None, lds, out[0].data_ptr(),
+            out[1].data_ptr(), raw)
+        if rc:
+            _moe._check(rc, "moe_add_rmsnorm_fp8")
+        return tuple(out)
+
+    def matmul(self, a, a_scale, b, b_scale, bias=None, residual=None, out=None, out_dtype=None, stream=None):
+        """``a @ b.T (+ bias) (+ residual)`` of 8-bit ``a [M, K]`` and ``b [N, K]``, rounded once to
+        ``out_dtype`` (bf16 by default, fp16 or fp32; ``out``'s or ``residual``'s where one is given).
+
+        ``bias``: bf16 ``[N]``; ``residual``: ``[M, N]`` of the output's type, which may be ``out`` itself.
+        K is a multiple of 16; rows of ``a`` at any distance of whole 16 bytes, of ``residual`` and ``out`` at any.
+        """
+        torch = self._torch
+        lda = self._rows(a, "a", (self._e4m3, torch.uint8))
+        M, K = a.shape
+        if b.dim() != 2:
+            _bad("matmul: b is a matrix")
+        N = b.shape[0]
+        self._codes_whole(b, "b", (N, K))
+        self._whole(a_scale, "a_scale", torch.float32, (M, _blocks(K)))
+        self._whole(b_scale, "b_scale", torch.float32, (_blocks(N), _blocks(K)))
+        if bias is not None:
+            self._whole(bias, "bias", torch.bfloat16, (N,))
+        if out_dtype is None:
+            out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.bfloat16
+        code = self._code.get(out_dtype)
+        if code is None:
+            _bad("matmul: outputs are bf16, fp16 or fp32, not %s" % out_dtype)
+        ldr = self._rows(residual, "residual", (out_dtype,), M, N) if residual is not None else 0
+        raw, where = self._on(stream)
+        if out is None:
+            out, = self._empty(where, ((M, N), out_dtype))
+        else:
+            if any(_overlap(out, t) for t in (a, a_scale, b, b_scale, bias)):
+                _bad("matmul: out overlaps an operand")
+            if _overlap(out, residual) and not _same_place(out, residual):
+                _bad("matmul: out overlaps residual without being it")
+        ldc = self._rows(out, "out", (out_dtype,), M, N)
+        rc = self._lib.moe_fp8_matmul(
+            self.ctx, M, N, K, a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+            bias.data_ptr() if bias is not None else None, residual.data_ptr() if residual is not None else None, ldr,
+            out.data_ptr(), ldc, code, raw)
+        if rc:
+            _moe._check(rc, "moe_fp8_matmul")
+        return out
+
+    def gated_matmul(self, a, a_scale, w13, w13_scale, bias=None, alpha: float = 1.702, limit: float = 7.0,
+                     shift: float = 1.0, stream=None):
+        """Both projections of a gated feed-forward block, its activation and the product: ``(h, h_scale)``,
+        ``h [M, F]`` in 8 bits for the block's second product.
+
+        ``w13``: ``[2 F, K]`` (or ``[2, F, K]``), gate rows, then linear rows; ``w13_scale``:
+        ``[2, ceil(F/128), ceil(K/128)]``; ``bias``: bf16 ``[2 F]``.  With ``g = min(gate, limit)`` and
+        ``u = clamp(linear, -limit, limit)``, ``h = g * sigmoid(alpha * g) * (u + shift)``: the experts'
+        activation by default, silu(gate) * linear for ``alpha=1, limit=math.inf, shift=0``.
+        """
+        torch = self._torch
+        lda = self._rows(a, "a", (self._e4m3, torch.uint8))
+        M, K = a.shape
+        F = w13.shape[0] // 2 if w13.dim() == 2 else w13.shape[1] if w13.dim() == 3 else 0
+        self._codes_whole(w13, "w13", (2 * F, K) if w13.dim() == 2 else (2, F, K))
+        self._whole(a_scale, "a_scale", torch.float32, (M, _blocks(K)))
+        self._whole(w13_scale, "w13_scale", torch.float32, (2, _blocks(F), _blocks(K)))
+        if bias is not None:
+            self._whole(bias, "bias", torch.bfloat16, (2 * F,))
+        raw, where = self._on(stream)
+        h, h_scale = self._empty(where, ((M, F), self._e4m3), ((M, _blocks(F)), torch.float32))
+        rc = self._lib.moe_fp8_gated_matmul(
+            self.ctx, M, F, K, a.data_ptr(), lda, a_scale.data_ptr(), w13.data_ptr(), w13_scale.data_ptr(),
+            bias.data_ptr() if bias is not None else None, alpha, limit, shift, h.data_ptr(), h_scale.data_ptr(), raw)
+        if rc:
+            _moe._check(rc, "moe_fp8_gated_matmul")
+        return h, h_scale
+
+    def sync_status(self, stream=None) -> int:
+        return moe_fp8_sync_status(self.ctx, stream)
+
+
+def _quantize(x, rows: int):
+    import torch
+    M, K = x.shape
+    b = torch.nn.functional.pad(x.float(), (0, -K % FP8_BLOCK, 0, -M % rows))
+    b = b.view(b.shape[0] // rows, rows, -1, FP8_BLOCK)
+    s = (b.abs().amax(dim=(1, 3)) / FP8_MAX).clamp_min(FP8_SCALE_MIN)
+    q = (b / s[:, None, :, None]).reshape(b.shape[0] * rows, -1)[:M, :K]
+    return q.to(torch.float8_e4m3fn).contiguous(), s.contiguous()
+
+
+def quantize_fp8_weight(w):
+    """A weight ``[N, K]`` in 8 bits: codes and a scale for each 128 x 128 block.  Done once, when weights are
+    loaded, so in elementary torch operations, on any device."""
+    return _quantize(w, FP8_BLOCK)
+
+
+def quantize_fp8_rows(x):
+    """Rows ``[M, K]`` in 8 bits: codes and a scale for each 128 elements, in elementary torch operations."""
+    return _quantize(x, 1)
+
+
+@dataclasses.dataclass
+class DenseWeights:
+    """The parameters of one dense feed-forward block, its matrices in 8 bits."""
+    norm_scale: "torch.Tensor"    # bf16 [d]
+    w13: "torch.Tensor"           # e4m3 [2F, d]: gate rows, then linear rows
+    w13_scale: "torch.Tensor"     # fp32 [2, ceil(F/128), ceil(d/128)]
+    b13: Optional["torch.Tensor"]  # bf16 [2F]
+    w2: "torch.Tensor"            # e4m3 [d, F]
+    w2_scale: "torch.Tensor"      # fp32 [ceil(d/128), ceil(F/128)]
+    b2: Optional["torch.Tensor"]  # bf16 [d]
+
+    @classmethod
+    def from_float(cls, norm_scale, w13, w2, b13=None, b2=None, device="cuda") -> "DenseWeights":
+        """From matrices in any floating type: ``w13 [2F, d]`` (gate rows, then linear rows), ``w2 [d, F]``."""
+        import torch
+        F = w13.shape[0] // 2
+        gate, linear = quantize_fp8_weight(w13[:F].to(device)), quantize_fp8_weight(w13[F:].to(device))
+        w2q, w2s = quantize_fp8_weight(w2.to(device))
+        bf16 = lambda t: None if t is None else t.to(device=device, dtype=torch.bfloat16).contiguous()  # noqa: E731
+        codes = torch.cat([gate[0].view(torch.uint8), linear[0].view(torch.uint8)]).view(torch.float8_e4m3fn)
+        return cls(bf16(norm_scale), codes, torch.stack([gate[1], linear[1]]), bf16(b13), w2q, w2s, bf16(b2))
+
+
+class DenseFFN:
+    """The dense (or shared-expert) counterpart of ``MoE``: RMSNorm, gated feed-forward, residual, three launches.
+
+    ``forward(x)`` is ``x + W2 h + b2`` with ``h`` the gated activation of ``W13 norm(x) + b13``;
+    ``forward(x, residual)`` takes ``x + residual`` in the place of ``x`` (a layer's pending addition).
+    """
+
+    def __init__(self, ops: Optional[Fp8Ops] = None, eps: float = 1e-5, alpha: float = 1.702, limit: float = 7.0,
+                 shift: float = 1.0):
+        self.ops = Fp8Ops() if ops is None else ops
+        self.eps, self.alpha, self.limit, self.shift = float(eps), float(alpha), float(limit), float(shift)
+
+    def forward(self, x, w: DenseWeights, residual=None, y=None, stream=None):
+        ops = self.ops
+        if residual is None:
+            q, s = ops.add_rmsnorm(x, w.norm_scale, eps=self.eps, stream=stream)
+            n = x
+        else:
+            q, s, n = ops.add_rmsnorm(x, w.norm_scale, residual=residual, eps=self.eps, stream=stream)
+        h, hs = ops.gated_matmul(q, s, w.w13, w.w13_scale, bias=w.b13, alpha=self.alpha, limit=self.limit,
+                                 shift=self.shift, stream=stream)
+        return ops.matmul(h, hs, w.w2, w.w2_scale, bias=w.b2, residual=n, out=y, out_dtype=x.dtype, stream=stream)
+
+    def sync_status(self, stream=None) -> int:
+        return self.ops.sync_status(stream)

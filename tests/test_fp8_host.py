@@ -1,0 +1,115 @@
+"""The dense 8-bit operators without a GPU: argument checks before any device work, the launch plan, the
+quantisers against their definition."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import sparse_moe_rmsnorm_b200 as moe
+from sparse_moe_rmsnorm_b200 import build as moe_build
+
+SM_SMEM, SM_TMEM = 228 * 1024, 512
+
+
+@pytest.fixture(scope="module")
+def lib():
+    moe_build.build()
+    return moe.lib()
+
+
+def test_null_context_and_null_results(lib):
+    assert lib.moe_fp8_init(None) == moe.MOE_ERR_ARG
+    assert lib.moe_fp8_destroy(None) == moe.MOE_OK
+    assert lib.moe_fp8_sync_status(None, None) == moe.MOE_ERR_ARG
+    assert lib.moe_fp8_set_wait_limit_ns(None, 5) == moe.MOE_ERR_ARG
+    assert lib.moe_add_rmsnorm_fp8(None, 1, 64, 0, None, 64, None, 0, None, 1e-5, None, 0, None, None, None) == moe.MOE_ERR_ARG
+    assert lib.moe_fp8_matmul(None, 1, 1, 16, None, 16, None, None, None, None, None, 0, None, 1, 0, None) == moe.MOE_ERR_ARG
+    assert lib.moe_fp8_gated_matmul(None, 1, 16, 16, None, 16, None, None, None, None, 1.0, 7.0, 1.0, None, None, None) == moe.MOE_ERR_ARG
+
+
+class Ctx(ctypes.Structure):
+    """The context's layout: enough to reach the argument checks, which use nothing of the device."""
+    _fields_ = [("device", ctypes.c_int), ("num_sms", ctypes.c_int), ("err", ctypes.c_void_p), ("limit", ctypes.c_ulonglong)]
+
+
+def test_sizes_types_strides_and_alignment(lib):
+    c = ctypes.byref(Ctx(0, 148, None, 1))
+    P = 1 << 20                                  # a pointer on every boundary; nothing reads it
+    norm = dict(T=4, d=64, type=0, x=P, ldx=64, r=None, ldr=0, w=P, eps=1e-5, sum=None, lds=0, q=P, s=P)
+    bad = [dict(T=-1), dict(d=0), dict(d=24), dict(d=16400), dict(type=3), dict(type=-1), dict(eps=-1.0), dict(eps=math.nan),
+           dict(x=None), dict(x=P + 8), dict(w=None), dict(w=P + 2), dict(q=P + 8), dict(q=None), dict(s=None), dict(s=P + 2),
+           dict(ldx=63), dict(ldx=68), dict(ldx=0), dict(r=P, ldr=32), dict(r=P + 4, ldr=64), dict(sum=P + 16, lds=12),
+           dict(sum=P, lds=128), dict(r=P + 4096, ldr=64, sum=P + 4096, lds=72)]
+    for b in bad:
+        v = {**norm, **b}
+        assert lib.moe_add_rmsnorm_fp8(c, v["T"], v["d"], v["type"], v["x"], v["ldx"], v["r"], v["ldr"], v["w"], v["eps"],
+                                       v["sum"], v["lds"], v["q"], v["s"], None) == moe.MOE_ERR_ARG, b
+    mm = dict(M=4, N=8, K=64, a=P, lda=64, sa=P, b=P, sb=P, bias=None, r=None, ldr=0, c=P, ldc=8, type=0)
+    bad = [dict(M=-1), dict(N=0), dict(K=0), dict(K=8), dict(K=72), dict(a=None), dict(a=P + 8), dict(lda=48), dict(lda=72),
+           dict(lda=1 << 40), dict(sa=None), dict(b=None), dict(b=P + 1), dict(sb=P + 1), dict(bias=P + 1), dict(c=None),
+           dict(c=P + 1), dict(ldc=7), dict(type=7), dict(r=P + 64, ldr=7), dict(r=P + 1, ldr=8), dict(r=P, ldr=16)]
+    for b in bad:
+        v = {**mm, **b}
+        assert lib.moe_fp8_matmul(c, v["M"], v["N"], v["K"], v["a"], v["lda"], v["sa"], v["b"], v["sb"], v["bias"], v["r"],
+                                  v["ldr"], v["c"], v["ldc"], v["type"], None) == moe.MOE_ERR_ARG, b
+    g = dict(M=4, F=32, K=64, a=P, lda=64, sa=P, b=P, sb=P, bias=None, alpha=1.0, limit=7.0, shift=1.0, h=P, hs=P)
+    bad = [dict(F=0), dict(F=40), dict(K=24), dict(M=-2), dict(limit=0.0), dict(limit=-1.0), dict(limit=math.nan),
+           dict(alpha=math.nan), dict(shift=math.nan), dict(h=None), dict(h=P + 4), dict(hs=P + 2), dict(b=P + 4), dict(lda=56)]
+    for b in bad:
+        v = {**g, **b}
+        assert lib.moe_fp8_gated_matmul(c, v["M"], v["F"], v["K"], v["a"], v["lda"], v["sa"], v["b"], v["sb"], v["bias"],
+                                        v["alpha"], v["limit"], v["shift"], v["h"], v["hs"], None) == moe.MOE_ERR_ARG, b
+    # no rows: nothing to do, whatever the pointers are
+    assert lib.moe_add_rmsnorm_fp8(c, 0, 64, 0, None, 0, None, 0, None, 1e-5, None, 0, None, None, None) == moe.MOE_OK
+    assert lib.moe_fp8_matmul(c, 0, 8, 64, None, 0, None, None, None, None, None, 0, None, 0, 0, None) == moe.MOE_OK
+    assert lib.moe_fp8_gated_matmul(c, 0, 32, 64, None, 0, None, None, None, None, 1.0, 7.0, 1.0, None, None, None) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M", [1, 7, 8, 9, 32, 64, 65, 128, 129, 255, 333, 1000, 2048, 8192, 100000])
+def test_plans_fit_and_cover(lib, gated, M):
+    """Whatever the sizes: the rings fit the shared memory taken; CTAs that fit an SM together find their TMEM
+    columns; the tiles cover every row and column; a cluster's CTAs share one 128-column block."""
+    for N in (16, 48, 128, 144, 1360, 2880, 5120, 20000):
+        for K in (16, 128, 144, 2880, 6144):
+            pl = moe.moe_fp8_debug_plan(gated, M, N, K, 148)
+            assert pl["smem_needed"] <= pl["smem"] <= 227 * 1024 and 2 <= pl["n_stages"] <= 16
+            per_sm = SM_SMEM // (pl["smem"] + 1024)
+            assert per_sm == pl["ctas_per_sm"] and per_sm * pl["tmem_cols"] <= SM_TMEM
+            # the share of TMEM is at most the share of shared memory, so any mix of variants fits too
+            assert pl["tmem_cols"] * SM_SMEM <= SM_TMEM * (pl["smem"] + 1024)
+            assert pl["a_rows"] % 8 == 0 and (pl["a_rows"] == 128 or M <= pl["a_rows"] < 128 and pl["m_tiles"] == 1)
+            assert pl["m_tiles"] * 128 * pl["ctas"] >= M > (pl["m_tiles"] - 1) * 128 * pl["ctas"]
+            n_tiles = pl["tiles"] // pl["m_tiles"]
+            assert n_tiles * pl["m_tiles"] == pl["tiles"]
+            width = 128 if gated else pl["bn"]
+            assert n_tiles * width >= N > (n_tiles - 1) * width
+            group = pl["ctas"] if pl["ctas"] > 1 else pl["cluster"]
+            assert pl["grid"] % group == 0 and 1 <= pl["grid"] <= 148 * per_sm and pl["grid"] // group <= pl["tiles"]
+            if gated and pl["bn"] < 256:
+                assert pl["cluster"] * pl["bn"] // 2 == 128
+
+
+def test_plan_rejects_bad_arguments(lib):
+    out = (ctypes.c_int * 12)()
+    for args in [(0, 0, 8, 64, 148), (0, 1, 0, 64, 148), (0, 1, 8, 60, 148), (0, 1, 8, 64, 0), (1, 1, 24, 64, 148),
+                 (0, 2 ** 31 - 1, 2 ** 31 - 1, 64, 148)]:
+        assert lib.moe_fp8_debug_plan(*args, out) == moe.MOE_ERR_ARG, args
+    assert lib.moe_fp8_debug_plan(0, 1, 8, 64, 148, None) == moe.MOE_ERR_ARG
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (5, 130), (200, 300)])
+def test_quantisers(M, K):
+    """A code times its scale is within half a step of the element; the scale is the block's maximum over 448."""
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)) * 3
+    x[0, :16] = 0
+    for (q, s), rows in ((moe.quantize_fp8_rows(x), 1), (moe.quantize_fp8_weight(x), 128)):
+        assert q.dtype == torch.float8_e4m3fn and q.shape == (M, K) and q.is_contiguous()
+        assert s.shape == (-(-M // rows), -(-K // 128)) and s.dtype == torch.float32
+        for i in range(s.shape[0]):
+            for j in range(s.shape[1]):
+                b = x[i * rows:(i + 1) * rows, 128 * j:128 * (j + 1)].double()
+                v = q[i * rows:(i + 1) * rows, 128 * j:128 * (j + 1)].double() * s[i, j].double()
+                assert abs(s[i, j].double() - max(b.abs().max() / 448, 2.0 ** -126)) <= 2.0 ** -23 * s[i, j].double()
+                assert ((v - b).abs() <= b.abs() * (2.0 ** -4 + 2.0 ** -22) + s[i, j].double() * 2.0 ** -10).all()
