@@ -1,4 +1,5 @@
-"""Build the sm_100a CUDA library ``libmoe_b200.so`` in-tree with nvcc.
+"""Build the sm_100a CUDA library ``libmoe_b200.so`` in-tree with nvcc, and ``_binding`` (its dense
+operators on torch tensors) with g++.
 
     python -m sparse_moe_rmsnorm_b200.build [--force] [--verbose]
 
@@ -13,12 +14,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
 HEADER = os.path.join(ROOT, "include", "moe_b200.h")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,16 +45,41 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def build(force: bool = False, verbose: bool = False, nvcc: str = "nvcc") -> str:
-    if not force and not _stale():
-        return LIB
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.dirname(HEADER), "-shared", "-o", tmp, *sources(), "-cudart", "static"]
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The torch extension over the library (which it links, and has to be there)."""
+    deps = [BINDING_SRC, HEADER, __file__]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    includes = [os.path.dirname(HEADER), sysconfig.get_paths()["include"],
+                *cpp_extension.include_paths(device_type="cuda")]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *[f for d in includes for f in ("-isystem", d)], "-o", tmp, BINDING_SRC,
+           "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
+           *["-L" + d for d in cpp_extension.library_paths(device_type="cuda")],
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
+def build(force: bool = False, verbose: bool = False, nvcc: str = "nvcc") -> str:
+    if force or _stale():
+        tmp = LIB + ".tmp.%d" % os.getpid()
+        cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.dirname(HEADER), "-shared", "-Xlinker",
+               "-soname=" + os.path.basename(LIB), "-o", tmp, *sources(), "-cudart", "static"]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
 
 

@@ -79,7 +79,7 @@ int product_params(moe_fp8_ctx *c, Fp8GemmParams &p, Fp8Plan &pl, int gated, int
                    long long lda, const float *a_scale, const uint8_t *b, const float *b_scale, const uint16_t *bias) {
     memset(&p, 0, sizeof p);
     if (!fp8_plan(M, N, K, gated, c->num_sms, &pl)) return MOE_ERR_ARG;
-    const int b_rows = gated ? pl.bn / 2 / fp8_wgs(pl.bn) : pl.bn / pl.ctas;
+    const int b_rows = gated ? pl.bn / 2 / fp8_wgs(pl.bn) : pl.bn / pl.ctas / fp8_split(pl.bn);
     if (!encode_u8(&p.map_a, a, K, M, lda, 1, pl.a_rows)) return MOE_ERR_ARG;
     if (!encode_u8(&p.map_b, b, K, N, K, gated ? 2 : 1, b_rows)) return MOE_ERR_ARG;
     p.a_scale = a_scale;

@@ -28,7 +28,7 @@ struct Fp8NormParams {
 
 struct Fp8GemmParams {
     CUtensorMap map_a;              // u8 {K, M, 1}, box {128, a_rows, 1}
-    CUtensorMap map_b;              // u8 {K, N, 1}, box {128, BN / CTAS, 1}; gated {K, F, 2}, box {128, half, 1}
+    CUtensorMap map_b;              // u8 {K, N, 1}, box {128, BN / CTAS / split, 1}; gated {K, F, 2}, box {128, h columns of a part, 1}
     const float *a_scale;           // [M, KB]
     const float *b_scale;           // [NB, KB]; gated [2, NB, KB]
     int M, N, K, KB, NB;            // N: output columns (gated: F)
@@ -63,18 +63,26 @@ constexpr int FP8_SMEM_SM = 227 * 1024; // shared memory of a CTA that has its S
 constexpr int FP8_SMEM_HALF = 113 * 1024;
 
 __host__ __device__ constexpr int fp8_wgs(int bn) { return bn >= 128 ? 2 : 1; }      // epilogue warpgroups
-__host__ __device__ constexpr int fp8_bufs(int bn) { return bn == 256 ? 2 : bn == 32 ? 8 : 4; }   // accumulators
+__host__ __device__ constexpr int fp8_bufs(int bn) { return bn == 256 ? 2 : bn == 32 ? 8 : 4; }   // accumulators of BN columns
+__host__ __device__ constexpr int fp8_split(int bn) { return bn == 256 ? 2 : 1; }   // parts that an accumulator fills and frees in
 // A variant takes its share of an SM's shared memory as it takes TMEM (512 or 256 of the 512
 // columns), whatever its rings need: CTAs that fit an SM together then find their TMEM columns
 // free, so no allocation waits while a CTA of the same cluster waits for it.
 __host__ __device__ constexpr int fp8_ctas_per_sm(int bn) { return fp8_bufs(bn) * bn == 512 ? 1 : 2; }
 __host__ __device__ constexpr int fp8_smem_bytes(int bn) { return fp8_ctas_per_sm(bn) == 1 ? FP8_SMEM_SM : FP8_SMEM_HALF; }
-__host__ __device__ constexpr int fp8_threads(int bn) { return fp8_wgs(bn) * 128 + 64; }
+__host__ __device__ constexpr int fp8_threads(int bn) { return fp8_wgs(bn) * 128 + (fp8_wgs(bn) > 1 ? 128 : 96); }
 
-// Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's 4 KB staging
-// tile, the barriers, the row maxima that warps or CTAs exchange, the TMEM base and abort flag.
+// The scales of FP8_CHUNK K blocks, as an epilogue warp keeps them in shared memory: per K block its
+// 32 rows' and the weight's (gated: both halves').  Two chunks per warp.
+constexpr int FP8_CHUNK = 4;
+constexpr int FP8_CHUNK_ROW = 36;       // words per K block: 32 rows, two weight scales, padding
+constexpr int FP8_TILE_BYTES = 32 * 64;    // an epilogue warp's staging tile: 32 rows of 64 bytes
+constexpr int FP8_CHUNK_BYTES = 2 * FP8_CHUNK * FP8_CHUNK_ROW * 4;
+
+// Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's staging
+// tile, each one's scales, the barriers, the row maxima that warps or CTAs exchange, the TMEM base and abort flag.
 struct Fp8Smem {
-    int a_stage, b_stage, b_off, stage_off, bar_off, ex_off, misc_off, total;
+    int a_stage, b_stage, b_off, stage_off, scale_off, bar_off, ex_off, misc_off, total;
 };
 
 __host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int cl, int gated, int a_rows, int n_stages) {
@@ -83,9 +91,11 @@ __host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int cl, int gated,
     s.b_stage = bn / ctas * FP8_KS;
     s.b_off = n_stages * s.a_stage;
     s.stage_off = s.b_off + n_stages * s.b_stage;
-    s.bar_off = s.stage_off + (gated ? 0 : fp8_wgs(bn) * 4 * 4096);
-    // full and empty per stage, full and empty per accumulator, drain, exchange [4 quarters][2 parities]
-    s.ex_off = s.bar_off + (2 * n_stages + 2 * fp8_bufs(bn) + 1 + 8) * 8;
+    s.scale_off = s.stage_off + (gated ? 0 : fp8_wgs(bn) * 4 * FP8_TILE_BYTES);
+    s.bar_off = s.scale_off + fp8_wgs(bn) * 4 * FP8_CHUNK_BYTES;
+    // full and empty per stage, full and empty per accumulator (part), drain [2 MMA warps], exchange
+    // [4 quarters][2 parities]
+    s.ex_off = s.bar_off + (2 * n_stages + 2 * fp8_split(bn) * fp8_bufs(bn) + 2 + 8) * 8;
     s.ex_off = (s.ex_off + 15) / 16 * 16;
     s.misc_off = s.ex_off + (gated ? 2 * (fp8_wgs(bn) > cl ? fp8_wgs(bn) : cl) * FP8_BM * 4 : 0);
     s.total = s.misc_off + 16;
@@ -98,15 +108,18 @@ __host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int cl, int gated,
 
 // The variant, ring depth and grid of one product.  Returns false when the sizes are out of range.
 inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, Fp8Plan *pl) {
-    const long long rows = (M + FP8_BM - 1) / FP8_BM;
+    long long rows = (M + FP8_BM - 1) / FP8_BM;
     auto cols = [&](int bn) -> long long { return gated ? fp8_blocks(N) : (N + bn - 1) / bn; };
-    pl->ctas = 1;
-    if (gated) {
+    pl->ctas = pl->cl = 1;
+    if (M > FP8_BM && (rows + 1) / 2 * cols(256) >= num_sms / 2) {
+        pl->bn = 256;
+        pl->ctas = 2;
+        rows = (rows + 1) / 2;
+    } else if (gated) {
         pl->bn = rows * cols(64) * 4 >= num_sms ? 64 : 32;
         pl->cl = FP8_BLOCK / (pl->bn / 2);
     } else {
         pl->bn = rows * cols(128) >= num_sms ? 128 : rows * cols(64) >= num_sms ? 64 : 32;
-        pl->cl = 1;
     }
     const long long tiles = rows * cols(pl->bn);
     if (tiles > (1 << 30)) return false;
@@ -115,8 +128,12 @@ inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, Fp8Plan *pl) {
     pl->a_rows = M < FP8_BM ? (M + 7) / 8 * 8 : FP8_BM;
     pl->tmem_cols = fp8_bufs(pl->bn) * pl->bn;
     pl->smem = fp8_smem_bytes(pl->bn);
+    // Where the two MMA warps take every other K block, an even number of stages keeps a stage with one
+    // of them: a warp that met only every other use of a barrier could take a phase for the one before
+    // or after it (a wait tells them apart by parity alone).
+    const int by = fp8_split(pl->bn) == 2 ? 1 : 2;
     int ns = FP8_STAGES_MAX;
-    while (ns > 2 && fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) --ns;
+    while (ns > 2 && fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) ns -= by;
     if (fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) return false;
     pl->n_stages = ns;
     const int group = pl->ctas == 2 ? 2 : pl->cl;

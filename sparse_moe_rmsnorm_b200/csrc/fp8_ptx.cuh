@@ -35,22 +35,38 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
+// The same without the cluster-scope release (which waits for all of the thread's memory operations):
+// for a barrier that orders tensor memory alone, after tcgen05.wait and its fence.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(hint_ns)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(hint_ns)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(hint_ns)
+            : "memory");
     return ok != 0;
 }
 
-// mbar_wait for a barrier that other CTAs of the cluster arrive on: acquires at cluster scope.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, const WaitCtl &w) {
+// The rest of a wait whose first sleep in the barrier unit has ended without the phase.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_phase_long(uint32_t bar, uint32_t parity, const WaitCtl &w) {
     const uint64_t start = globaltimer_ns();
     for (;;) {
-        if (mbar_try_wait_cluster(bar, parity, MBAR_SUSPEND_HINT_NS)) return true;
+        if (try_phase<CLUSTER>(bar, parity, MBAR_SUSPEND_HINT_NS)) return true;
         if (*w.abort) return false;
         if (globaltimer_ns() - start > w.limit_ns) {
             *w.abort = 1;
@@ -60,18 +76,44 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// Bounded wait as mbar_wait, by any thread.  The limit's start is taken after the first sleep (1 ms), so
+// an ordinary wait reads no timer.  CLUSTER: other CTAs arrive on the barrier; acquires at cluster scope.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    if (try_phase<CLUSTER>(bar, parity, MBAR_SUSPEND_HINT_NS)) return true;
+    return wait_phase_long<CLUSTER>(bar, parity, w);
+}
+
 // --------------------------------------------------------------------- TMA
 
-// A 3-D box into this CTA's shared memory whose bytes are counted on the barrier of the
+// A 3-D box into this CTA's shared memory.  CTAS == 2: its bytes are counted on the barrier of the
 // pair's even CTA (the barrier's address with the CTA bit cleared).
-__device__ __forceinline__ void tma_load_3d_pair_w(void *dst, const void *map, uint64_t *bar, int c0, int c1,
-                                                   int c2) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%3, %4, %5}], [%2];\n\t}" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(smem_addr(bar) & 0xFEFFFFFFu), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
+template <int CTAS>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, uint32_t bar, int c0, int c1, int c2) {
+    if constexpr (CTAS == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+            "%5}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+            "{%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar & 0xFEFFFFFFu), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(e));
+    return e != 0;
 }
 
 // ----------------------------------------------------------------- tcgen05
@@ -101,38 +143,45 @@ __device__ __forceinline__ void tmem_dealloc_g(uint32_t taddr, uint32_t ncols) {
 
 // D[tmem] (+)= A[smem] * B[smem]^T, E4M3 operands, fp32 accumulators; K = 32.
 template <int CTAS>
-__device__ __forceinline__ void mma_f8_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
     if constexpr (CTAS == 1)
         asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
             : "memory");
 }
 
 // Arrive on `bar` (CTAS == 2: the barrier at this address in both CTAs of the pair) once the
-// MMAs issued before have completed.
+// MMAs this thread issued before have completed.
 template <int CTAS>
-__device__ __forceinline__ void mma_commit_g(uint64_t *bar) {
+__device__ __forceinline__ void mma_commit_g(uint32_t bar) {
     if constexpr (CTAS == 1)
-        mma_commit_w(bar);
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync r|e, 0xffffffff;\n\t"
-            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
-            ::"r"(smem_addr(bar))
+            "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+            ::"r"(bar)
             : "memory");
 }
 
-// Each thread of the warp reads 32 consecutive 32-bit columns of its lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Each thread of the warp reads N (16 or 32) consecutive 32-bit columns of its lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]);
+
+template <>
+__device__ __forceinline__ void tmem_ld<16>(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+
+template <>
+__device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -144,10 +193,26 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
+// Four bytes from global to shared memory, asynchronously, in groups.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // max(a, b), NaN where either is.
 __device__ __forceinline__ float fmax_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float fmin_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 

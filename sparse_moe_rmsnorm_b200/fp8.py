@@ -5,9 +5,9 @@ A matrix in 8 bits is a pair of tensors: E4M3 codes (``torch.float8_e4m3fn``, or
 of a row (``[M, ceil(K/128)]``), weights ``[N, K]`` one for each 128 x 128 block
 (``[ceil(N/128), ceil(K/128)]``).
 
-Like the rest of the package this only checks and marshals arguments: the work is in the CUDA
-library, every call raises where the library or a B200 is missing, and a call returns when its kernel
-is queued.
+Like the rest of the package this only checks and marshals arguments (``Fp8Ops`` does so in C++,
+``csrc/binding.cpp``): the work is in the CUDA library, every call raises where the library or a B200
+is missing, and a call returns when its kernel is queued.
 """
 from __future__ import annotations
 
@@ -87,46 +87,44 @@ def moe_fp8_debug_plan(gated: bool, M: int, N: int, K: int, num_sms: int) -> Dic
 
 # ------------------------------------------------------------- torch layer
 
-def _blocks(n: int) -> int:
-    return -(-n // FP8_BLOCK)
+_binding_module = None
 
 
-def _bad(what: str) -> None:
-    raise _moe.MoEError(_moe.MOE_ERR_ARG, what)
+def _binding():
+    """The operators on torch tensors (``csrc/binding.cpp``): checks, output allocation and the C call."""
+    global _binding_module
+    if _binding_module is None:
+        import importlib
 
-
-def _overlap(a, b) -> bool:
-    """Whether the byte ranges of two tensors meet."""
-    def span(t):
-        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-        return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-    if a is None or b is None or not a.numel() or not b.numel():
-        return False
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
-
-
-def _same_place(a, b) -> bool:
-    return b is not None and a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        _moe.lib()
+        try:
+            mod = importlib.import_module("sparse_moe_rmsnorm_b200._binding")
+        except ImportError as e:
+            raise RuntimeError("the torch binding is not built; run `python -m sparse_moe_rmsnorm_b200.build`") from e
+        mod.set_error(_moe.MoEError)
+        _binding_module = mod
+    return _binding_module
 
 
 class Fp8Ops:
     """The operators on one device.  One object serves any number of streams and captured graphs at once;
-    make it (and every shape's first call is like any other) outside a capture."""
+    make it outside a capture.
+
+    ``stream``: where a call runs (a ``torch.cuda.Stream`` or a raw handle), by default the device's current
+    one; outputs that the call allocates belong to it.
+    """
 
     def __init__(self, device=None):
         import torch
         dev = torch.device("cuda" if device is None else device)
         if dev.type != "cuda":
-            _bad("Fp8Ops: not a CUDA device")
+            raise _moe.MoEError(_moe.MOE_ERR_ARG, "Fp8Ops: not a CUDA device")
         self._index = torch.cuda.current_device() if dev.index is None else dev.index
         self.device = torch.device("cuda", self._index)
+        self._c = _binding()
         with torch.cuda.device(self._index):
             self.ctx = moe_fp8_init()
-        self._lib = _moe.lib()
-        self._torch = torch
-        self._code = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
-        self._e4m3 = torch.float8_e4m3fn
 
     def close(self) -> None:
         if getattr(self, "ctx", None):
@@ -139,46 +137,11 @@ class Fp8Ops:
         except Exception:
             pass
 
-    # -- argument checks ---------------------------------------------------
-
-    def _rows(self, t, name, dtypes, rows=None, cols=None):
-        """The row distance of a matrix of this device whose rows are contiguous."""
-        if t.dim() != 2 or t.dtype not in dtypes or t.get_device() != self._index:
-            _bad("%s: a matrix of %s on %s is wanted, got %s %s on %s"
-                 % (name, " or ".join(map(str, dtypes)), self.device, tuple(t.shape), t.dtype, t.device))
-        r, c = t.shape
-        if (rows is not None and r != rows) or (cols is not None and c != cols):
-            _bad("%s: %s x %s is wanted, got %d x %d" % (name, rows, cols, r, c))
-        if c > 1 and t.stride(1) != 1:
-            _bad("%s: the elements of a row have to be contiguous" % name)
-        return t.stride(0) if r > 1 else -(-c // 16) * 16     # one row has no distance to the next
-
-    def _whole(self, t, name, dtype, shape):
-        """A contiguous tensor of this device."""
-        if t.dtype != dtype or tuple(t.shape) != shape or t.get_device() != self._index or not t.is_contiguous():
-            _bad("%s: a contiguous %s %s on %s is wanted, got %s %s on %s"
-                 % (name, dtype, shape, self.device, tuple(t.shape), t.dtype, t.device))
-
-    def _codes_whole(self, t, name, shape):
-        self._whole(t, name, t.dtype if t.dtype in (self._e4m3, self._torch.uint8) else self._e4m3, shape)
-
     def _on(self, stream):
-        """(raw stream, context in which outputs are allocated): they belong to the stream that fills them."""
-        torch = self._torch
-        if stream is None:
-            return torch.cuda.current_stream(self._index).cuda_stream, None
+        import torch
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
-        return stream.cuda_stream, torch.cuda.stream(stream)
-
-    def _empty(self, where, *spec):
-        torch = self._torch
-        if where is None:
-            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in spec]
-        with where:
-            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in spec]
-
-    # -- operators ---------------------------------------------------------
+        return torch.cuda.stream(stream)
 
     def add_rmsnorm(self, x, norm_scale, residual=None, eps: float = 1e-5, sum_out=None, stream=None):
         """RMS norm of ``x + residual`` (of ``x`` without one) in 8 bits: ``(q, q_scale, sum)``, without a
@@ -188,39 +151,10 @@ class Fp8Ops:
         ``norm_scale``: bf16 ``[d]``.  ``sum`` is ``x + residual`` in their type, written to ``sum_out`` if
         given, which may be ``x`` or ``residual``.
         """
-        torch = self._torch
-        code = self._code.get(x.dtype)
-        if code is None:
-            _bad("add_rmsnorm: x is bf16, fp16 or fp32, got %s" % x.dtype)
-        ldx = self._rows(x, "x", (x.dtype,))
-        T, d = x.shape
-        self._whole(norm_scale, "norm_scale", torch.bfloat16, (d,))
-        ldr = lds = 0
-        if residual is not None:
-            ldr = self._rows(residual, "residual", (x.dtype,), T, d)
-        elif sum_out is not None:
-            _bad("add_rmsnorm: there is no sum without a residual")
-        raw, where = self._on(stream)
-        spec = [((T, d), self._e4m3), ((T, _blocks(d)), torch.float32)]
-        if residual is not None and sum_out is None:
-            spec.append(((T, d), x.dtype))
-        out = self._empty(where, *spec)
-        if sum_out is not None:
-            for t in (x, residual):
-                if _overlap(sum_out, t) and not _same_place(sum_out, t):
-                    _bad("add_rmsnorm: sum_out overlaps an input without being it")
-            if _overlap(sum_out, norm_scale):
-                _bad("add_rmsnorm: sum_out overlaps norm_scale")
-            out.append(sum_out)
-        if residual is not None:
-            lds = self._rows(out[2], "sum_out", (x.dtype,), T, d)
-        rc = self._lib.moe_add_rmsnorm_fp8(
-            self.ctx, T, d, code, x.data_ptr(), ldx, residual.data_ptr() if residual is not None else None, ldr,
-            norm_scale.data_ptr(), eps, out[2].data_ptr() if residual is not None else None, lds, out[0].data_ptr(),
-            out[1].data_ptr(), raw)
-        if rc:
-            _moe._check(rc, "moe_add_rmsnorm_fp8")
-        return tuple(out)
+        if stream is not None:
+            with self._on(stream):
+                return self._c.add_rmsnorm(self.ctx, self._index, x, norm_scale, residual, eps, sum_out)
+        return self._c.add_rmsnorm(self.ctx, self._index, x, norm_scale, residual, eps, sum_out)
 
     def matmul(self, a, a_scale, b, b_scale, bias=None, residual=None, out=None, out_dtype=None, stream=None):
         """``a @ b.T (+ bias) (+ residual)`` of 8-bit ``a [M, K]`` and ``b [N, K]``, rounded once to
@@ -229,39 +163,10 @@ class Fp8Ops:
         ``bias``: bf16 ``[N]``; ``residual``: ``[M, N]`` of the output's type, which may be ``out`` itself.
         K is a multiple of 16; rows of ``a`` at any distance of whole 16 bytes, of ``residual`` and ``out`` at any.
         """
-        torch = self._torch
-        lda = self._rows(a, "a", (self._e4m3, torch.uint8))
-        M, K = a.shape
-        if b.dim() != 2:
-            _bad("matmul: b is a matrix")
-        N = b.shape[0]
-        self._codes_whole(b, "b", (N, K))
-        self._whole(a_scale, "a_scale", torch.float32, (M, _blocks(K)))
-        self._whole(b_scale, "b_scale", torch.float32, (_blocks(N), _blocks(K)))
-        if bias is not None:
-            self._whole(bias, "bias", torch.bfloat16, (N,))
-        if out_dtype is None:
-            out_dtype = out.dtype if out is not None else residual.dtype if residual is not None else torch.bfloat16
-        code = self._code.get(out_dtype)
-        if code is None:
-            _bad("matmul: outputs are bf16, fp16 or fp32, not %s" % out_dtype)
-        ldr = self._rows(residual, "residual", (out_dtype,), M, N) if residual is not None else 0
-        raw, where = self._on(stream)
-        if out is None:
-            out, = self._empty(where, ((M, N), out_dtype))
-        else:
-            if any(_overlap(out, t) for t in (a, a_scale, b, b_scale, bias)):
-                _bad("matmul: out overlaps an operand")
-            if _overlap(out, residual) and not _same_place(out, residual):
-                _bad("matmul: out overlaps residual without being it")
-        ldc = self._rows(out, "out", (out_dtype,), M, N)
-        rc = self._lib.moe_fp8_matmul(
-            self.ctx, M, N, K, a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
-            bias.data_ptr() if bias is not None else None, residual.data_ptr() if residual is not None else None, ldr,
-            out.data_ptr(), ldc, code, raw)
-        if rc:
-            _moe._check(rc, "moe_fp8_matmul")
-        return out
+        if stream is not None:
+            with self._on(stream):
+                return self._c.matmul(self.ctx, self._index, a, a_scale, b, b_scale, bias, residual, out, out_dtype)
+        return self._c.matmul(self.ctx, self._index, a, a_scale, b, b_scale, bias, residual, out, out_dtype)
 
     def gated_matmul(self, a, a_scale, w13, w13_scale, bias=None, alpha: float = 1.702, limit: float = 7.0,
                      shift: float = 1.0, stream=None):
@@ -273,23 +178,10 @@ class Fp8Ops:
         ``u = clamp(linear, -limit, limit)``, ``h = g * sigmoid(alpha * g) * (u + shift)``: the experts'
         activation by default, silu(gate) * linear for ``alpha=1, limit=math.inf, shift=0``.
         """
-        torch = self._torch
-        lda = self._rows(a, "a", (self._e4m3, torch.uint8))
-        M, K = a.shape
-        F = w13.shape[0] // 2 if w13.dim() == 2 else w13.shape[1] if w13.dim() == 3 else 0
-        self._codes_whole(w13, "w13", (2 * F, K) if w13.dim() == 2 else (2, F, K))
-        self._whole(a_scale, "a_scale", torch.float32, (M, _blocks(K)))
-        self._whole(w13_scale, "w13_scale", torch.float32, (2, _blocks(F), _blocks(K)))
-        if bias is not None:
-            self._whole(bias, "bias", torch.bfloat16, (2 * F,))
-        raw, where = self._on(stream)
-        h, h_scale = self._empty(where, ((M, F), self._e4m3), ((M, _blocks(F)), torch.float32))
-        rc = self._lib.moe_fp8_gated_matmul(
-            self.ctx, M, F, K, a.data_ptr(), lda, a_scale.data_ptr(), w13.data_ptr(), w13_scale.data_ptr(),
-            bias.data_ptr() if bias is not None else None, alpha, limit, shift, h.data_ptr(), h_scale.data_ptr(), raw)
-        if rc:
-            _moe._check(rc, "moe_fp8_gated_matmul")
-        return h, h_scale
+        if stream is not None:
+            with self._on(stream):
+                return self._c.gated_matmul(self.ctx, self._index, a, a_scale, w13, w13_scale, bias, alpha, limit, shift)
+        return self._c.gated_matmul(self.ctx, self._index, a, a_scale, w13, w13_scale, bias, alpha, limit, shift)
 
     def sync_status(self, stream=None) -> int:
         return moe_fp8_sync_status(self.ctx, stream)

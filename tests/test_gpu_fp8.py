@@ -93,7 +93,7 @@ def test_norm_zeros_infinities_and_nan(ops):
 
 SIZES = [(1, 1, 16), (1, 5, 32), (3, 16, 48), (8, 33, 128), (9, 31, 144), (32, 64, 256), (33, 65, 272), (64, 127, 400),
          (65, 129, 640), (127, 128, 1040), (128, 257, 128), (129, 255, 2064), (255, 130, 512), (257, 300, 784),
-         (1, 5120, 2880), (17, 2885, 2880), (300, 1000, 4112), (1000, 2880, 576), (2049, 1303, 304)]
+         (1, 5120, 2880), (17, 2885, 2880), (300, 1000, 4112), (1000, 2880, 576), (2049, 1303, 304), (256, 5120, 2880), (200, 4901, 784)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
