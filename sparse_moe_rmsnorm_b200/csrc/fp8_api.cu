@@ -13,6 +13,7 @@
 namespace moe {
 cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, cudaStream_t s);
 cudaError_t fp8_gemm_setup();
+cudaError_t launch_fp8_few(const Fp8FewParams &p, int gated, cudaStream_t s);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s);
 }  // namespace moe
 
@@ -97,6 +98,24 @@ int product_params(moe_fp8_ctx *c, Fp8GemmParams &p, Fp8Plan &pl, int gated, int
     p.err = c->err;
     p.wait_limit_ns = c->wait_limit_ns;
     return MOE_OK;
+}
+
+Fp8FewParams few_params(int M, int N, int K, const uint8_t *a, long long lda, const float *a_scale, const uint8_t *b,
+                        const float *b_scale, const uint16_t *bias) {
+    Fp8FewParams p;
+    memset(&p, 0, sizeof p);
+    p.a = a;
+    p.b = b;
+    p.a_scale = a_scale;
+    p.b_scale = b_scale;
+    p.bias = bias;
+    p.lda = lda;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.KB = fp8_blocks(K);
+    p.NB = fp8_blocks(N);
+    return p;
 }
 
 }  // namespace
@@ -206,6 +225,15 @@ int moe_fp8_matmul(moe_fp8_ctx_t *c, int M, int N, int K, const uint8_t *a, int6
     if (residual == out && ldr != ldc) return MOE_ERR_ARG;
     DeviceGuard g(c->device);
     if (!g.ok) return MOE_ERR_CUDA;
+    if (fp8_few(M, N, 0, c->num_sms)) {
+        Fp8FewParams p = few_params(M, N, K, a, lda, a_scale, b, b_scale, bias);
+        p.residual = residual;
+        p.ldr = ldr;
+        p.c = out;
+        p.ldc = ldc;
+        p.type = type;
+        return status(launch_fp8_few(p, 0, static_cast<cudaStream_t>(stream)));
+    }
     Fp8GemmParams p;
     Fp8Plan pl;
     if ((rc = product_params(c, p, pl, 0, M, N, K, a, lda, a_scale, b, b_scale, bias))) return rc;
@@ -214,8 +242,7 @@ int moe_fp8_matmul(moe_fp8_ctx_t *c, int M, int N, int K, const uint8_t *a, int6
     p.c = out;
     p.ldc = ldc;
     p.type = type;
-    p.vec_c = aligned(out, 16) && ldc * eb % 16 == 0;
-    p.vec_r = residual && aligned(residual, 16) && ldr * eb % 16 == 0;
+    p.vec = aligned(out, 4 * eb) && ldc % 4 == 0 && (!residual || (aligned(residual, 4 * eb) && ldr % 4 == 0));
     return status(launch_fp8_gemm(p, pl, 0, static_cast<cudaStream_t>(stream)));
 }
 
@@ -228,6 +255,15 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
     if (!aligned(h, 16) || !aligned(h_scale, 4)) return MOE_ERR_ARG;
     DeviceGuard g(c->device);
     if (!g.ok) return MOE_ERR_CUDA;
+    if (fp8_few(M, F, 1, c->num_sms)) {
+        Fp8FewParams p = few_params(M, F, K, a, lda, a_scale, w13, w13_scale, b13);
+        p.alpha = alpha;
+        p.limit = limit;
+        p.shift = shift;
+        p.h = h;
+        p.h_scale = h_scale;
+        return status(launch_fp8_few(p, 1, static_cast<cudaStream_t>(stream)));
+    }
     Fp8GemmParams p;
     Fp8Plan pl;
     if ((rc = product_params(c, p, pl, 1, M, F, K, a, lda, a_scale, w13, w13_scale, b13))) return rc;

@@ -17,7 +17,9 @@
 // warps (or, for narrow tiles, the CTAs of a cluster, through distributed shared memory).
 //
 // Warp roles: 4 or 8 epilogue warps (warp w reads TMEM lane quarter w % 4), then the TMA
-// producer, then two MMA warps, one elected lane of each running its loop.
+// producer, then two MMA warps, one elected lane of each running its loop, then
+// the warp that fetches the scales (16 K blocks ahead: loads of them in the epilogue's loop put a
+// round trip to L2 on every block).
 // Persistent: CTAs (clusters) walk the output tiles, rows fastest, so the B tile of neighbouring
 // CTAs is the same and A stays in L2.
 //
@@ -40,138 +42,109 @@ constexpr unsigned int FP8_ERR_WAIT = 1u;
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
-// A warp's staging tile: 32 rows of 64 bytes, 16-byte piece p of row r at slot p ^ (r / 2 & 3), so that
-// the eight lanes of a 128-byte access meet in no bank, whether they hold one piece of eight rows or
-// two rows' pieces.
-__device__ __forceinline__ uint4 *piece(uint8_t *stage, int r, int p) {
-    return reinterpret_cast<uint4 *>(stage + r * 64 + ((p ^ (r >> 1 & 3)) << 4));
-}
-
-// Between the staging tile and rows of global memory, PCS pieces to a row: PCS neighbouring lanes take
-// a row, so its bytes move together.  At the edges, and where rows do not start on 16 bytes, element
-// by element.
-template <typename T, int PCS, bool STORE>
-__device__ __forceinline__ void move_tile(uint8_t *stage, T *g, long long ld, int rows, int cols, bool vec, int lane) {
-    constexpr int VEC = 16 / sizeof(T);
-    const int pc = lane % PCS, r0 = lane / PCS;
-    T *at = g + r0 * ld + pc * VEC;
-    if (vec && rows == 32 && cols == PCS * VEC) {
-#pragma unroll
-        for (int it = 0; it < PCS; ++it) {
-            uint4 *slot = piece(stage, it * (32 / PCS) + r0, pc);
-            if constexpr (STORE) *reinterpret_cast<uint4 *>(at) = *slot;
-            else *slot = *reinterpret_cast<const uint4 *>(at);
-            at += (32 / PCS) * ld;
-        }
-        return;
-    }
-#pragma unroll 1
-    for (int r = r0; r < rows; r += 32 / PCS, at += (32 / PCS) * ld) {
-        uint4 *slot = piece(stage, r, pc);
-        if (vec && (pc + 1) * VEC <= cols) {
-            if constexpr (STORE) *reinterpret_cast<uint4 *>(at) = *slot;
-            else *slot = *reinterpret_cast<const uint4 *>(at);
+// V elements (1 or 4) of type T.
+template <typename T, int V>
+struct Pack {
+    typename std::conditional<V == 1, T, typename std::conditional<sizeof(T) == 4, uint4, uint2>::type>::type raw;
+    __device__ __forceinline__ float get(int j) const { return static_cast<float>(reinterpret_cast<const T *>(&raw)[j]); }
+    __device__ __forceinline__ void set(const float (&v)[V]) {
+        if constexpr (V == 4 && std::is_same<T, __half>::value) {
+            reinterpret_cast<__half2 *>(&raw)[0] = __floats2half2_rn(v[0], v[1]);
+            reinterpret_cast<__half2 *>(&raw)[1] = __floats2half2_rn(v[2], v[3]);
+        } else if constexpr (V == 4 && std::is_same<T, __nv_bfloat16>::value) {
+            reinterpret_cast<__nv_bfloat162 *>(&raw)[0] = __floats2bfloat162_rn(v[0], v[1]);
+            reinterpret_cast<__nv_bfloat162 *>(&raw)[1] = __floats2bfloat162_rn(v[2], v[3]);
         } else {
-            T *e = reinterpret_cast<T *>(slot);
+#pragma unroll
+            for (int j = 0; j < V; ++j) reinterpret_cast<T *>(&raw)[j] = static_cast<T>(v[j]);
+        }
+    }
+};
+
+// The staged sums (+ bias) (+ residual), rounded once, to rows m0.. and columns n0.. of c; lane i brings the
+// bias of column n0 + i.  V == 4: 32 whole rows, four elements per lane; V == 1: what there is, a column per
+// lane.  Four steps at a time, their residuals first; every element of the residual is read by the thread that
+// writes c's, so the two may be the same.
+template <typename T, int CC, int V, bool RES>
+__device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *tile, float bias, int m0, int n0, int lane) {
+    constexpr int LPR = CC / V, RPI = 32 / LPR;              // lanes per row, rows per step
+    typedef decltype(Pack<T, V>::raw) Raw;
+    const int pc = lane % LPR, r0 = lane / LPR, col = n0 + V * pc;
+    float b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = __shfl_sync(0xffffffffu, bias, V * pc + j);
+    const int rows = V == 4 ? 32 : col < p.N ? min(32, p.M - m0) : 0;
+    T *c = static_cast<T *>(p.c) + (long long)(m0 + r0) * p.ldc + col;
+    const T *res = RES ? static_cast<const T *>(p.residual) + (long long)(m0 + r0) * p.ldr + col : nullptr;
+    const long long cs = RPI * p.ldc, rs = RPI * p.ldr;
+    const float *f = tile + r0 * (CC + 4) + V * pc;
 #pragma unroll 1
-            for (int j = 0; j < VEC && pc * VEC + j < cols; ++j) {
-                if constexpr (STORE) at[j] = e[j];
-                else e[j] = at[j];
-            }
-        }
-    }
-}
-
-// The eight or four elements of a piece, rounded (with RES: added to what the piece holds).
-template <typename T, bool RES>
-__device__ __forceinline__ uint4 pack_piece(const float *v, const uint4 &old) {
-    uint4 u;
-    if constexpr (sizeof(T) == 4) {
-        float4 f = make_float4(v[0], v[1], v[2], v[3]);
+    for (int r = r0; r < rows; r += 4 * RPI, f += 4 * RPI * (CC + 4)) {
+        Pack<T, V> old[4];
         if constexpr (RES) {
-            f.x += __uint_as_float(old.x), f.y += __uint_as_float(old.y);
-            f.z += __uint_as_float(old.z), f.w += __uint_as_float(old.w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i, res += rs)
+                if (V == 4 || r + i * RPI < rows) old[i].raw = *reinterpret_cast<const Raw *>(res);
         }
-        u = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
-    } else {
-        const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float a = v[2 * i], b = v[2 * i + 1];
-            if constexpr (RES) {
-                const T *e = reinterpret_cast<const T *>(&o[i]);
-                a += static_cast<float>(e[0]), b += static_cast<float>(e[1]);
-            }
-            if constexpr (std::is_same<T, __half>::value) {
-                const __half2 h = __floats2half2_rn(a, b);
-                w[i] = *reinterpret_cast<const uint32_t *>(&h);
-            } else {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                w[i] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-        }
-        u = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return u;
-}
-
-// c = sums (+ residual), rounded once: CW columns of 32 rows, each thread's row to the staging tile in
-// 16-byte pieces, then out of it row by row.
-template <typename T, int CW, bool RES>
-__device__ __forceinline__ void store_columns(const Fp8GemmParams &p, const float (&acc)[CW], uint8_t *stage, int m0,
-                                              int n0, int lane) {
-    constexpr int VEC = 16 / sizeof(T);
-    constexpr int PCS = CW / VEC < 4 ? CW / VEC : 4;
-    const int rows = min(32, p.M - m0);
-    T *c = static_cast<T *>(p.c) + (long long)m0 * p.ldc + n0;
-    T *res = const_cast<T *>(static_cast<const T *>(p.residual)) + (RES ? (long long)m0 * p.ldr + n0 : 0);
+        for (int i = 0; i < 4; ++i, c += cs) {
+            if (V == 4 || r + i * RPI < rows) {
+                float o[V];
+                if constexpr (V == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(f + i * RPI * (CC + 4));
+                    o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+                } else {
+                    o[0] = f[i * RPI * (CC + 4)];
+                }
 #pragma unroll
-    for (int c0 = 0; c0 < CW; c0 += PCS * VEC) {
-        const int cols = min(PCS * VEC, p.N - n0 - c0);
-        if (cols > 0) {
-            if constexpr (RES) {
-                move_tile<T, PCS, false>(stage, res + c0, p.ldr, rows, cols, p.vec_r, lane);
-                __syncwarp();
+                for (int j = 0; j < V; ++j) {
+                    o[j] += b[j];
+                    if constexpr (RES) o[j] += old[i].get(j);
+                }
+                Pack<T, V> out;
+                out.set(o);
+                *reinterpret_cast<Raw *>(c) = out.raw;
             }
-#pragma unroll
-            for (int pc = 0; pc < PCS; ++pc) {
-                uint4 *slot = piece(stage, lane, pc);
-                uint4 old = make_uint4(0, 0, 0, 0);
-                if constexpr (RES) old = *slot;
-                *slot = pack_piece<T, RES>(acc + c0 + pc * VEC, old);
-            }
-            __syncwarp();
-            move_tile<T, PCS, true>(stage, c + c0, p.ldc, rows, cols, p.vec_c, lane);
-            __syncwarp();
         }
     }
 }
 
-template <typename T, int CW>
-__device__ __forceinline__ void store_columns(const Fp8GemmParams &p, const float (&acc)[CW], uint8_t *stage, int m0,
-                                              int n0, int lane) {
-    if (p.residual) store_columns<T, CW, true>(p, acc, stage, m0, n0, lane);
-    else store_columns<T, CW, false>(p, acc, stage, m0, n0, lane);
+template <typename T, int CC>
+__device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *tile, float bias, int m0, int n0, int lane) {
+    if (p.vec && m0 + 32 <= p.M && n0 + CC <= p.N) {
+        if (p.residual) put_tile<T, CC, 4, true>(p, tile, bias, m0, n0, lane);
+        else put_tile<T, CC, 4, false>(p, tile, bias, m0, n0, lane);
+    } else {
+        if (p.residual) put_tile<T, CC, 1, true>(p, tile, bias, m0, n0, lane);
+        else put_tile<T, CC, 1, false>(p, tile, bias, m0, n0, lane);
+    }
 }
 
-// v[0 .. n) = bias[0 .. n) (zeros past `valid`, and without a bias).
-template <int N>
-__device__ __forceinline__ void load_bias(float *v, const uint16_t *bias, int valid) {
-    if (bias && valid >= N && (reinterpret_cast<uintptr_t>(bias) & 15) == 0) {
+// A warp's sums, CC columns at a time: each thread's row into the staging tile, rows out of it.  The loop over
+// the parts stays a loop (its body is every part's): code that runs once a tile does not stay in the
+// instruction caches, and unrolled for each type it took longer to fetch than to run.
+template <int CW, int CC>
+__device__ __forceinline__ void store_columns(const Fp8GemmParams &p, const float (&acc)[CW], const float (&bias)[(CW + 31) / 32],
+                                              float *tile, int m0, int n0, int lane) {
+#pragma unroll 1
+    for (int part = 0; part < CW / CC; ++part) {
+        if (n0 + part * CC >= p.N) break;
+        float b = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(bias + i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int s = 0; s < CW / CC; ++s)
+            if (s == part) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[i + 2 * j] = __uint_as_float(w[j] << 16);
-                v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                for (int i = 0; i < CC; i += 4)
+                    *reinterpret_cast<float4 *>(tile + lane * (CC + 4) + i) =
+                        make_float4(acc[s * CC + i], acc[s * CC + i + 1], acc[s * CC + i + 2], acc[s * CC + i + 3]);
+                b = bias[s * CC / 32];
             }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = bias && i < valid ? bf16_bits_to_f32(bias[i]) : 0.0f;
+        if (CC < 32) b = __shfl_sync(0xffffffffu, b, (part * CC + lane) % 32);     // this part's columns from lane 0 on
+        __syncwarp();
+        if (p.type == FP8_BF16) put_tile<__nv_bfloat16, CC>(p, tile, b, m0, n0 + part * CC, lane);
+        else if (p.type == FP8_FP16) put_tile<__half, CC>(p, tile, b, m0, n0 + part * CC, lane);
+        else put_tile<float, CC>(p, tile, b, m0, n0 + part * CC, lane);
+        __syncwarp();
     }
 }
 
@@ -189,7 +162,8 @@ template <int BN, int CTAS, bool GATED, int CL>
 __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr int WGS = fp8_wgs(BN);            // epilogue warpgroups
     constexpr int CW = BN / WGS;                // accumulator columns per epilogue thread
-    constexpr int LD = CW > 64 ? 32 : 16;       // columns of a TMEM load (registers: 2 LD beside the CW sums)
+    constexpr int LD = 16;                      // columns of a TMEM load (registers: 2 LD beside the CW sums)
+    constexpr int CC = fp8_tile_cols(BN);       // columns of a staging tile
     constexpr int HW = CW / 2;                  // gated: h columns per thread
     constexpr int BUFS = fp8_bufs(BN);
     constexpr int SPLIT = fp8_split(BN);        // parts of an accumulator: one per warpgroup, or the whole
@@ -208,13 +182,16 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
     uint64_t *d_empty = d_full + SPLIT * BUFS;  // ... and has been read
     uint64_t *drain_bar = d_empty + SPLIT * BUFS;   // [2 MMA warps]
     uint64_t *ex_bar = drain_bar + 2;           // [4 quarters][2 parities]
+    uint64_t *sc_full = ex_bar + 8;             // [FP8_CHUNKS] a chunk of scales is there
+    uint64_t *sc_empty = sc_full + FP8_CHUNKS;  // ... and has been read
+    const uint32_t scales0 = smem_addr(smem + plan.scale_off);
     float *ex = reinterpret_cast<float *>(smem + plan.ex_off);       // [2 parities][EX][128 rows]
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + plan.misc_off);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + plan.misc_off + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CSIZE > 1 ? cluster_ctarank() : 0;
-    constexpr int TMA_WARP = WGS * 4, MMA_WARP = TMA_WARP + 1;
+    constexpr int TMA_WARP = WGS * 4, MMA_WARP = TMA_WARP + 1, SCALE_WARP = TMA_WARP + 3;
     constexpr uint32_t COLS = BUFS * BN;
 
     if (threadIdx.x == 0) {
@@ -229,6 +206,10 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
         mbar_init(&drain_bar[0], 1);
         mbar_init(&drain_bar[1], 1);
         for (int i = 0; i < 8; ++i) mbar_init(&ex_bar[i], EX);
+        for (int i = 0; i < FP8_CHUNKS; ++i) {
+            mbar_init(&sc_full[i], 32);         // every lane of the scale warp
+            mbar_init(&sc_empty[i], WGS * 4);   // every epilogue warp
+        }
         *abort_s = 0;
         fence_barrier_init();
     }
@@ -325,6 +306,40 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                 mma_commit_g<CTAS>(smem_addr(&drain_bar[m]));
                 wait_drain(&drain_bar[m], 0, p.wait_limit_ns);
             }
+        } else if (warp == SCALE_WARP) {
+            // The scales, a chunk of K blocks at a time: four neighbouring lanes take a row's four blocks.
+            const int k = lane % FP8_CHUNK, r0 = lane / FP8_CHUNK;
+            constexpr int RPI = 32 / FP8_CHUNK;                 // rows per instruction
+            const uint32_t full0 = smem_addr(sc_full), empty0 = smem_addr(sc_empty);
+            const uint32_t dst0 = scales0 + (uint32_t)lane * 4;
+            int cb = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int t = first; t < p.tiles && ok; t += step) {
+                const int nt = t / p.m_tiles;
+                const int m0 = (t - nt * p.m_tiles) * (FP8_BM * CTAS) + (CTAS == 2 ? (int)rank * FP8_BM : 0);
+                const int rows = p.M - m0 - r0;                 // this lane's first row is there if > 0
+                const float *sa = p.a_scale + (long long)(m0 + r0) * p.KB + k;
+                const long long next = (long long)RPI * p.KB;
+                // the weight's scales: gated, the gate's and the linear part's; else each warpgroup's block
+                const int blk = (GATED ? nt * FP8_BLOCK : nt * BN + r0 * CW) / FP8_BLOCK;
+                const bool has_b = r0 < (GATED ? 2 : WGS) && blk < p.NB;
+                const float *sb = p.b_scale + ((long long)(GATED ? r0 * p.NB : 0) + blk) * p.KB + k;
+                for (int kb = 0; kb < p.KB; kb += FP8_CHUNK) {
+                    if (!__all_sync(0xffffffffu, wait_phase<false>(empty0 + 8u * cb, ph ^ 1, wc))) { ok = false; break; }
+                    const uint32_t dst = dst0 + (uint32_t)(cb * FP8_CHUNK_BYTES);
+                    if (kb + k < p.KB) {
+                        const float *src = sa + kb;
+#pragma unroll
+                        for (int i = 0; i < FP8_BM / RPI; ++i, src += next)
+                            if (i * RPI < rows) cp_async4(dst + i * 128, src);
+                        if (has_b) cp_async4(dst + FP8_BM * FP8_CHUNK * 4, sb + kb);      // behind the rows
+                    }
+                    cp_async_arrive(full0 + 8u * cb);
+                    if (++cb == FP8_CHUNKS) { cb = 0; ph ^= 1; }
+                }
+            }
+            cp_async_wait_all();
         }
     } else {
         if constexpr (WGS > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -333,103 +348,89 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(SPLIT == 2 ? wg * BUFS * PN : wg * CW);
         const uint32_t d_full0 = smem_addr(d_full + part * BUFS);
         const uint32_t d_empty0 = CTAS == 2 ? map_to_rank(smem_addr(d_empty + part * BUFS), 0) : smem_addr(d_empty);
+        const uint32_t sc_full0 = smem_addr(sc_full), sc_empty0 = smem_addr(sc_empty);
         int buf = 0, par = 0, cb = 0;
-        uint32_t dph = 0, exph = 0;
+        uint32_t dph = 0, exph = 0, cph = 0;
         bool ok = true;
-        // first row and column of the warp's part of tile t
-        auto place = [&](int t, int &m0, int &n0) {
-            const int nt = t / p.m_tiles;
-            m0 = (t % p.m_tiles) * (FP8_BM * CTAS) + (CTAS == 2 ? (int)rank * FP8_BM : 0) + 32 * q;
-            n0 = GATED ? nt * FP8_BLOCK + (WGS > 1 ? wg : (int)rank) * HW : nt * BN + wg * CW;
-        };
-        // The scales come a chunk of K blocks ahead (the next tile's first chunk during this one's
-        // last), asynchronously: a load per block and row in the loop below put an L2 round trip on
-        // every block.  Neighbouring lanes take a row's blocks of the chunk.
-        float *scales = reinterpret_cast<float *>(smem + plan.scale_off + warp * FP8_CHUNK_BYTES);
-        auto fetch = [&](int t, int kb0, int into) {
-            if (t < p.tiles) {
-                int m0, n0;
-                place(t, m0, n0);
-                const uint32_t dst = smem_addr(scales + into * FP8_CHUNK * FP8_CHUNK_ROW);
-                const int k = lane % FP8_CHUNK, kb = kb0 + k;
-                if (kb < p.KB) {
-#pragma unroll
-                    for (int i = 0; i < FP8_CHUNK; ++i) {
-                        const int r = i * (32 / FP8_CHUNK) + lane / FP8_CHUNK;
-                        if (m0 + r < p.M)
-                            cp_async4(dst + (uint32_t)(k * FP8_CHUNK_ROW + r) * 4, p.a_scale + (long long)(m0 + r) * p.KB + kb);
-                    }
-                    const int half = lane / FP8_CHUNK;
-                    if (half < (GATED ? 2 : 1) && n0 < p.N)
-                        cp_async4(dst + (uint32_t)(k * FP8_CHUNK_ROW + 32 + half) * 4,
-                                  p.b_scale + ((long long)half * p.NB + n0 / FP8_BLOCK) * p.KB + kb);
-                }
+        const int KB = p.KB;
+        auto release = [&](uint32_t bar) {          // the warp has read its columns of an accumulator
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CTAS == 2) mbar_arrive_remote(bar);
+                else mbar_arrive_at(bar);
             }
-            cp_async_commit();
         };
-        fetch(first, 0, 0);
         for (int t = first; t < p.tiles && ok; t += step) {
-            int m0, n0;
-            place(t, m0, n0);
+            // first row and column of the warp's part of the tile
+            const int nt = t / p.m_tiles;
+            const int m0 = (t - nt * p.m_tiles) * (FP8_BM * CTAS) + (CTAS == 2 ? (int)rank * FP8_BM : 0) + 32 * q;
+            const int n0 = GATED ? nt * FP8_BLOCK + (WGS > 1 ? wg : (int)rank) * HW : nt * BN + wg * CW;
             const bool active = m0 < p.M && n0 < p.N;      // the warp has something to write
-            float acc[CW];
-            if constexpr (GATED) {
-                load_bias<HW>(acc, p.bias ? p.bias + n0 : nullptr, p.N - n0);
-                load_bias<HW>(acc + HW, p.bias ? p.bias + p.N + n0 : nullptr, p.N - n0);
-            } else {
-                load_bias<CW>(acc, p.bias ? p.bias + n0 : nullptr, p.N - n0);
+            // lane i: the biases of the columns 32 j + i (gated: of the gate, then of the linear part), read
+            // here so that they have arrived when the sums are complete
+            float bias[(CW + 31) / 32];
+#pragma unroll
+            for (int j = 0; j < (CW + 31) / 32; ++j) {
+                const int i = 32 * j + lane, col = n0 + (GATED ? i % HW : i);
+                bias[j] = p.bias && i < CW && col < p.N ? bf16_bits_to_f32(p.bias[(GATED && i >= HW ? p.N : 0) + col]) : 0.0f;
             }
-            for (int kb = 0; kb < p.KB; ++kb) {
-                const int k = kb % FP8_CHUNK;
-                if (k == 0) {
-                    __syncwarp();               // the buffer's last readers are done
-                    fetch(kb + FP8_CHUNK < p.KB ? t : t + step, kb + FP8_CHUNK < p.KB ? kb + FP8_CHUNK : 0, cb ^ 1);
-                    cp_async_wait<1>();
-                    __syncwarp();
-                    cb ^= 1;
-                }
-                const float *sc = scales + ((cb ^ 1) * FP8_CHUNK + k) * FP8_CHUNK_ROW;
-                const float sa = sc[lane], s0 = sa * sc[32], s1 = GATED ? sa * sc[33] : s0;
-                if (!__all_sync(0xffffffffu, wait_phase<false>(d_full0 + 8u * buf, dph, wc))) { ok = false; break; }
-                tc_fence_after();
-                auto release = [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CTAS == 2) mbar_arrive_remote(d_empty0 + 8u * (uint32_t)buf);
-                        else mbar_arrive(&d_empty[buf]);
-                    }
-                };
-                if (active) {
-                    // the next LD columns are on their way while these are added
-                    const uint32_t from = lane_base + (uint32_t)(buf * PN);
-                    uint32_t r[2][LD];
-                    tmem_ld<LD>(from, r[0]);
+            float acc[CW];
 #pragma unroll
-                    for (int c = 0; c < CW; c += LD) {
-                        tmem_wait_ld();
-                        if (c + LD < CW) tmem_ld<LD>(from + (uint32_t)(c + LD), r[(c / LD + 1) & 1]);
-                        else release();
+            for (int i = 0; i < CW; ++i) acc[i] = 0.0f;
+            for (int kb = 0; kb < KB; kb += FP8_CHUNK) {
+                wait_phase_through(sc_full0 + 8u * cb, cph, wc);
+                const float *sc = reinterpret_cast<const float *>(smem + plan.scale_off + cb * FP8_CHUNK_BYTES);
+                const float *sa = sc + (32 * q + lane) * FP8_CHUNK, *sb = sc + (FP8_BM + (GATED ? 0 : wg)) * FP8_CHUNK;
+                const int blocks = min(FP8_CHUNK, KB - kb);
+#pragma unroll 1
+                for (int k = 0; k < blocks; ++k) {
+                    const float s0 = sa[k] * sb[k], s1 = GATED ? sa[k] * sb[FP8_CHUNK + k] : 0.0f;
+                    const uint32_t freed = d_empty0 + 8u * buf;
+                    wait_phase_through(d_full0 + 8u * buf, dph, wc);
+                    tc_fence_after();
+                    if (active) {
+                        // the next LD columns are on their way while these are added
+                        const uint32_t from = lane_base + (uint32_t)(buf * PN);
+                        uint32_t r[2][LD];
+                        tmem_ld<LD>(from, r[0]);
 #pragma unroll
-                        for (int i = 0; i < LD; ++i)
-                            acc[c + i] = fmaf(__uint_as_float(r[(c / LD) & 1][i]), GATED && c + i >= HW ? s1 : s0, acc[c + i]);
+                        for (int c = 0; c < CW; c += LD) {
+                            tmem_wait_ld();
+                            if (c + LD < CW) tmem_ld<LD>(from + (uint32_t)(c + LD), r[(c / LD + 1) & 1]);
+                            else release(freed);
+#pragma unroll
+                            for (int i = 0; i < LD; ++i)
+                                acc[c + i] = fmaf(__uint_as_float(r[(c / LD) & 1][i]), GATED && c + i >= HW ? s1 : s0, acc[c + i]);
+                        }
+                    } else {
+                        release(freed);
                     }
-                } else {
-                    release();
+                    if (++buf == BUFS) { buf = 0; dph ^= 1; }
                 }
-                if (++buf == BUFS) { buf = 0; dph ^= 1; }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(sc_empty0 + 8u * cb);
+                if (++cb == FP8_CHUNKS) { cb = 0; cph ^= 1; }
+                if (__any_sync(0xffffffffu, *abort_s)) { ok = false; break; }
             }
             if (!ok) break;
             if constexpr (GATED) {
                 const int row = 32 * q + lane;
-                float amax = 0.0f;
+                const float minus_alpha_log2e = -1.44269504f * p.alpha;
+                float amax = 0.0f, h[HW];
+                const float *bs = reinterpret_cast<const float *>(smem + plan.stage_off + warp * fp8_tile_bytes(BN, 1));
+#pragma unroll
+                for (int j = 0; j < (CW + 31) / 32; ++j)
+                    if (32 * j + lane < CW) const_cast<float *>(bs)[32 * j + lane] = bias[j];
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < HW; ++i) {
-                    const float g = fmin_nan(acc[i], p.limit);
-                    const float u = fmax_nan(fmin_nan(acc[HW + i], p.limit), -p.limit);
-                    acc[i] = __fdividef(g, 1.0f + __expf(-p.alpha * g)) * (u + p.shift);
-                    if (n0 + i < p.N) amax = fmax_nan(amax, fabsf(acc[i]));
+                    const float g = fmin_nan(acc[i] + bs[i], p.limit);
+                    const float u = fmax_nan(fmin_nan(acc[HW + i] + bs[HW + i], p.limit), -p.limit);
+                    h[i] = g * rcp_approx(1.0f + exp2_approx(minus_alpha_log2e * g)) * (u + p.shift);
+                    if (n0 + i < p.N) amax = fmax_nan(amax, fabsf(h[i]));
                 }
+                __syncwarp();
                 // the row's maximum over its 128-column block
                 float *slot = ex + (par * EX) * FP8_BM + row;
                 uint64_t *bar = &ex_bar[2 * q + par];
@@ -453,29 +454,25 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                 if (active && m0 + lane < p.M) {
                     const float s = fmax_nan(amax / FP8_MAX, FP8_SCALE_MIN);
                     const float inv = 1.0f / s;
-                    uint8_t *h = p.h + (long long)(m0 + lane) * p.N + n0;
+                    uint8_t *to = p.h + (long long)(m0 + lane) * p.N + n0;
 #pragma unroll
                     for (int i = 0; i < HW; i += 16)
                         if (n0 + i < p.N) {
-                            uint4 u;
-                            u.x = f32x4_to_e4m3x4(acc[i] * inv, acc[i + 1] * inv, acc[i + 2] * inv, acc[i + 3] * inv);
-                            u.y = f32x4_to_e4m3x4(acc[i + 4] * inv, acc[i + 5] * inv, acc[i + 6] * inv, acc[i + 7] * inv);
-                            u.z = f32x4_to_e4m3x4(acc[i + 8] * inv, acc[i + 9] * inv, acc[i + 10] * inv, acc[i + 11] * inv);
-                            u.w = f32x4_to_e4m3x4(acc[i + 12] * inv, acc[i + 13] * inv, acc[i + 14] * inv, acc[i + 15] * inv);
-                            *reinterpret_cast<uint4 *>(h + i) = u;
+                            uint32_t u[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                u[j] = f32x4_to_e4m3x4(h[i + 4 * j] * inv, h[i + 4 * j + 1] * inv, h[i + 4 * j + 2] * inv,
+                                                       h[i + 4 * j + 3] * inv);
+                            *reinterpret_cast<uint4 *>(to + i) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     if (n0 % FP8_BLOCK == 0) p.h_scale[(long long)(m0 + lane) * p.NB + n0 / FP8_BLOCK] = s;
                 }
             } else if (active) {
-                uint8_t *stage = smem + plan.stage_off + warp * FP8_TILE_BYTES;
-                if (p.type == FP8_BF16) store_columns<__nv_bfloat16, CW>(p, acc, stage, m0, n0, lane);
-                else if (p.type == FP8_FP16) store_columns<__half, CW>(p, acc, stage, m0, n0, lane);
-                else store_columns<float, CW>(p, acc, stage, m0, n0, lane);
+                store_columns<CW, CC>(p, acc, bias, reinterpret_cast<float *>(smem + plan.stage_off + warp * fp8_tile_bytes(BN, 0)), m0, n0, lane);
             }
         }
     }
 
-    cp_async_wait<0>();
     __syncwarp();
     tc_fence_before();
     __syncthreads();

@@ -39,12 +39,32 @@ struct Fp8GemmParams {
     void *c;                        // type [M, N], rows ldc elements apart
     long long ldr, ldc;
     int type;                       // FP8_BF16, FP8_FP16 or FP8_FP32
-    int vec_c, vec_r;               // rows of c / of the residual start on 16 bytes
+    int vec;                        // four elements of a row of c (and of the residual) move as one
     float alpha, limit, shift;      // gated activation
     uint8_t *h;                     // gated: E4M3 [M, F]
     float *h_scale;                 // gated: [M, NB]
     unsigned int *err;
     unsigned long long wait_limit_ns;
+};
+
+// The same products for up to FP8_FEW rows (fp8_few.cu).
+constexpr int FP8_FEW = 16;
+constexpr int FP8_FEW_CTAS = 3;         // CTAs (16 columns each) to an SM, at most
+inline bool fp8_few(int M, int N, int gated, int num_sms) {
+    const long long ctas = gated ? fp8_blocks(N) * 8LL : (N + 15LL) / 16;
+    return M <= FP8_FEW && ctas <= (long long)(gated ? 2 : FP8_FEW_CTAS) * num_sms;
+}
+struct Fp8FewParams {
+    const uint8_t *a, *b;           // E4M3 [M, K] (rows lda bytes apart), [N, K] (gated [2, F, K])
+    const float *a_scale, *b_scale;
+    const uint16_t *bias;
+    const void *residual;
+    void *c;
+    uint8_t *h;
+    float *h_scale;
+    long long lda, ldr, ldc;
+    int M, N, K, KB, NB, type;
+    float alpha, limit, shift;
 };
 
 // One kernel variant: BN columns of accumulators per CTA (gated: BN / 2 gate and BN / 2 linear
@@ -70,17 +90,23 @@ __host__ __device__ constexpr int fp8_split(int bn) { return bn == 256 ? 2 : 1; 
 // free, so no allocation waits while a CTA of the same cluster waits for it.
 __host__ __device__ constexpr int fp8_ctas_per_sm(int bn) { return fp8_bufs(bn) * bn == 512 ? 1 : 2; }
 __host__ __device__ constexpr int fp8_smem_bytes(int bn) { return fp8_ctas_per_sm(bn) == 1 ? FP8_SMEM_SM : FP8_SMEM_HALF; }
-__host__ __device__ constexpr int fp8_threads(int bn) { return fp8_wgs(bn) * 128 + (fp8_wgs(bn) > 1 ? 128 : 96); }
+__host__ __device__ constexpr int fp8_threads(int bn) { return fp8_wgs(bn) * 128 + 128; }
 
-// The scales of FP8_CHUNK K blocks, as an epilogue warp keeps them in shared memory: per K block its
-// 32 rows' and the weight's (gated: both halves').  Two chunks per warp.
-constexpr int FP8_CHUNK = 4;
-constexpr int FP8_CHUNK_ROW = 36;       // words per K block: 32 rows, two weight scales, padding
-constexpr int FP8_TILE_BYTES = 32 * 64;    // an epilogue warp's staging tile: 32 rows of 64 bytes
-constexpr int FP8_CHUNK_BYTES = 2 * FP8_CHUNK * FP8_CHUNK_ROW * 4;
+// The scales on their way to the epilogue: a ring of chunks of four K blocks, in a chunk a row's four
+// scales side by side, for the CTA's 128 rows and two of the weight's blocks (each warpgroup's, or the
+// gate's and the linear part's).
+constexpr int FP8_CHUNK = 4, FP8_CHUNKS = 4;
+constexpr int FP8_CHUNK_BYTES = (FP8_BM + 2) * FP8_CHUNK * 4;
+constexpr int FP8_SCALE_BYTES = FP8_CHUNKS * FP8_CHUNK_BYTES;
+// An epilogue warp's staging tile: 32 rows of 32 or 16 sums, rows 16 bytes further apart than they are long
+// (gated: the biases of its columns).
+__host__ __device__ constexpr int fp8_tile_cols(int bn) { return fp8_wgs(bn) > 1 ? 32 : 16; }
+__host__ __device__ constexpr int fp8_tile_bytes(int bn, int gated) {
+    return gated ? bn / fp8_wgs(bn) * 4 : 32 * (fp8_tile_cols(bn) + 4) * 4;
+}
 
 // Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's staging
-// tile, each one's scales, the barriers, the row maxima that warps or CTAs exchange, the TMEM base and abort flag.
+// tile, the scales, the barriers, the row maxima that warps or CTAs exchange, the TMEM base and abort flag.
 struct Fp8Smem {
     int a_stage, b_stage, b_off, stage_off, scale_off, bar_off, ex_off, misc_off, total;
 };
@@ -91,11 +117,11 @@ __host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int cl, int gated,
     s.b_stage = bn / ctas * FP8_KS;
     s.b_off = n_stages * s.a_stage;
     s.stage_off = s.b_off + n_stages * s.b_stage;
-    s.scale_off = s.stage_off + (gated ? 0 : fp8_wgs(bn) * 4 * FP8_TILE_BYTES);
-    s.bar_off = s.scale_off + fp8_wgs(bn) * 4 * FP8_CHUNK_BYTES;
+    s.scale_off = s.stage_off + fp8_wgs(bn) * 4 * fp8_tile_bytes(bn, gated);     // a multiple of 16
+    s.bar_off = s.scale_off + FP8_SCALE_BYTES;
     // full and empty per stage, full and empty per accumulator (part), drain [2 MMA warps], exchange
-    // [4 quarters][2 parities]
-    s.ex_off = s.bar_off + (2 * n_stages + 2 * fp8_split(bn) * fp8_bufs(bn) + 2 + 8) * 8;
+    // [4 quarters][2 parities], full and empty per chunk of scales
+    s.ex_off = s.bar_off + (2 * n_stages + 2 * fp8_split(bn) * fp8_bufs(bn) + 2 + 8 + 2 * FP8_CHUNKS) * 8;
     s.ex_off = (s.ex_off + 15) / 16 * 16;
     s.misc_off = s.ex_off + (gated ? 2 * (fp8_wgs(bn) > cl ? fp8_wgs(bn) : cl) * FP8_BM * 4 : 0);
     s.total = s.misc_off + 16;

@@ -14,8 +14,11 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // The shared::cluster address of this CTA's shared address `a` in CTA `rank` of the cluster.
@@ -33,6 +36,10 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 // thread's earlier writes at cluster scope.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The same without the cluster-scope release (which waits for all of the thread's memory operations):
@@ -74,6 +81,13 @@ __device__ __forceinline__ bool wait_phase_long(uint32_t bar, uint32_t parity, c
             return false;
         }
     }
+}
+
+// wait_phase for the lanes of a warp that stays converged: a wait that runs out sets the abort flag and
+// returns like any other; the warp looks at the flag where it can leave together.
+__device__ __forceinline__ void wait_phase_through(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    if (!try_phase<false>(bar, parity, MBAR_SUSPEND_HINT_NS)) wait_phase_long<false>(bar, parity, w);
+    __syncwarp();
 }
 
 // Bounded wait as mbar_wait, by any thread.  The limit's start is taken after the first sleep (1 ms), so
@@ -193,15 +207,15 @@ __device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
-// Four bytes from global to shared memory, asynchronously, in groups.
+// Four bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+// Arrive on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // max(a, b), NaN where either is.
 __device__ __forceinline__ float fmax_nan(float a, float b) {
@@ -213,6 +227,18 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
 __device__ __forceinline__ float fmin_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 2^x and 1 / x by the hardware's approximations (2 and 1 units in the last place; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
