@@ -285,8 +285,8 @@ MOE_API int moe_fp8_sync_status(moe_fp8_ctx_t *ctx, void *stream);
 MOE_API int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *ctx, unsigned long long ns);
 
 /* n = x + residual (residual may be NULL: n = x), in fp32;
- * sum_out = n rounded to `type` (may be NULL; may be x or residual themselves,
- * with the same row distance);
+ * sum_out = n rounded to `type` (may be NULL, and is without a residual; may be x
+ * or residual themselves, with the same row distance);
  * q, q_scale = n / sqrt(mean(n^2) + eps) * norm_scale in E4M3.
  * x, residual, sum_out: type [T, d], rows ldx / ldr / lds elements apart (whole
  * 16-byte units); norm_scale bf16 [d]; q u8 [T, d]; q_scale fp32 [T, ceil(d/128)].

@@ -11,7 +11,7 @@
 #include "host_plan.cuh"
 
 namespace moe {
-cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, cudaStream_t s);
+cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, int num_sms, cudaStream_t s);
 cudaError_t fp8_gemm_setup();
 cudaError_t launch_fp8_few(const Fp8FewParams &p, int gated, cudaStream_t s);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s);
@@ -192,6 +192,7 @@ int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *c, int T, int d, int type, const void *x,
         !aligned(q, 16) || !aligned(q_scale, 4))
         return MOE_ERR_ARG;
     const int row = 16 / eb;
+    if (sum_out && !residual) return MOE_ERR_ARG;      // the sum is x
     if (ldx < d || ldx % row || (residual && (ldr < d || ldr % row)) || (sum_out && (lds < d || lds % row)))
         return MOE_ERR_ARG;
     // a row's sum replaces x or the residual in place, or lies elsewhere
@@ -211,7 +212,7 @@ int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *c, int T, int d, int type, const void *x,
     p.T = T;
     p.d = d;
     p.eps = eps;
-    return status(launch_add_rmsnorm_fp8(p, type, static_cast<cudaStream_t>(stream)));
+    return status(launch_add_rmsnorm_fp8(p, type, c->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_fp8_matmul(moe_fp8_ctx_t *c, int M, int N, int K, const uint8_t *a, int64_t lda, const float *a_scale,
