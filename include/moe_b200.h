@@ -267,7 +267,8 @@ MOE_API int moe_forward_noalloc(int T, int d_model, int d_ff, int n_experts, int
  *
  * No call allocates or keeps anything: there is no workspace, and calls on one
  * context may overlap (streams, host threads, captured graphs).  Results do not
- * depend on timing: the same inputs give the same bits.  Outputs must not
+ * depend on timing: the same inputs give the same bits.  Rows, columns and K are
+ * at most 2^30.  Outputs must not
  * overlap inputs except where stated.  The context's device is made current
  * during a call; pointers and stream belong to it. */
 
@@ -315,10 +316,11 @@ MOE_API int moe_fp8_gated_matmul(moe_fp8_ctx_t *ctx, int M, int F, int K, const 
                          const float *a_scale, const uint8_t *w13, const float *w13_scale, const uint16_t *b13,
                          float alpha, float limit, float shift, uint8_t *h, float *h_scale, void *stream);
 
-/* The launch plan of moe_fp8_matmul (gated 0) or moe_fp8_gated_matmul (gated 1, N = F),
- * computed on the host alone.  Writes out[0..11] = {accumulator columns per CTA, CTAs per MMA,
- * CTAs sharing a gated block, rows of an A stage, stages, row tiles, tiles, grid, shared
- * memory taken, shared memory needed, TMEM columns, CTAs per SM}.  For tests of the planner. */
+/* The launch plan of moe_fp8_matmul (gated 0) or moe_fp8_gated_matmul (gated 1, N = F) for
+ * num_sms SMs, computed on the host alone.  Writes out[0..9] = {whether the kernel for a few rows
+ * takes it (the rest is then what the other would do), accumulator columns per CTA, CTAs per MMA,
+ * CTAs that split K, rows of an A stage, stages, row tiles, tiles, grid, shared memory needed}.
+ * For tests of the planner. */
 MOE_API int moe_fp8_debug_plan(int gated, int M, int N, int K, int num_sms, int *out);
 
 /* A human-readable name of an error code. */

@@ -12,7 +12,7 @@
 
 namespace moe {
 cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, int num_sms, cudaStream_t s);
-cudaError_t fp8_gemm_setup();
+cudaError_t fp8_gemm_setup(int *clusters);
 cudaError_t launch_fp8_few(const Fp8FewParams &p, int gated, cudaStream_t s);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s);
 }  // namespace moe
@@ -26,6 +26,7 @@ struct moe_fp8_ctx {
     int num_sms;
     unsigned int *err;
     unsigned long long wait_limit_ns;
+    int clusters[FP8_SPLIT_MAX + 1];    // clusters of n CTAs that the device holds at once
 };
 
 namespace {
@@ -67,7 +68,8 @@ bool encode_u8(CUtensorMap *m, const void *base, int K, long long rows, long lon
 
 int check_product(moe_fp8_ctx *c, int M, int N, int K, const uint8_t *a, long long lda, const float *a_scale,
                   const uint8_t *b, const float *b_scale, const uint16_t *bias) {
-    if (!c || M < 0 || N < 1 || K < 16 || K % 16) return MOE_ERR_ARG;
+    if (!c || M < 0 || N < 1 || K < 16 || K % 16 || M > FP8_SIZE_MAX || N > FP8_SIZE_MAX || K > FP8_SIZE_MAX)
+        return MOE_ERR_ARG;
     if (M == 0) return MOE_OK;
     if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(b, 16) || !aligned(b_scale, 4) || !aligned_or_null(bias, 2))
         return MOE_ERR_ARG;
@@ -79,8 +81,8 @@ int check_product(moe_fp8_ctx *c, int M, int N, int K, const uint8_t *a, long lo
 int product_params(moe_fp8_ctx *c, Fp8GemmParams &p, Fp8Plan &pl, int gated, int M, int N, int K, const uint8_t *a,
                    long long lda, const float *a_scale, const uint8_t *b, const float *b_scale, const uint16_t *bias) {
     memset(&p, 0, sizeof p);
-    if (!fp8_plan(M, N, K, gated, c->num_sms, &pl)) return MOE_ERR_ARG;
-    const int b_rows = gated ? pl.bn / 2 / fp8_wgs(pl.bn) : pl.bn / pl.ctas / fp8_split(pl.bn);
+    if (!fp8_plan(M, N, K, gated, c->num_sms, c->clusters, &pl)) return MOE_ERR_ARG;
+    const int b_rows = gated ? pl.bn / 4 : pl.bn / pl.ctas / fp8_split(pl.bn);
     if (!encode_u8(&p.map_a, a, K, M, lda, 1, pl.a_rows)) return MOE_ERR_ARG;
     if (!encode_u8(&p.map_b, b, K, N, K, gated ? 2 : 1, b_rows)) return MOE_ERR_ARG;
     p.a_scale = a_scale;
@@ -94,6 +96,7 @@ int product_params(moe_fp8_ctx *c, Fp8GemmParams &p, Fp8Plan &pl, int gated, int
     p.tiles = pl.tiles;
     p.a_rows = pl.a_rows;
     p.n_stages = pl.n_stages;
+    p.split = pl.split;
     p.bias = bias;
     p.err = c->err;
     p.wait_limit_ns = c->wait_limit_ns;
@@ -132,12 +135,17 @@ int moe_fp8_init(moe_fp8_ctx_t **out) {
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (major != 10 || minor != 0) return MOE_ERR_UNSUPPORTED;
-    if (!encode_fn() || fp8_gemm_setup() != cudaSuccess) return MOE_ERR_CUDA;
+    if (!encode_fn()) return MOE_ERR_CUDA;
     moe_fp8_ctx *c = new (std::nothrow) moe_fp8_ctx;
     if (!c) return MOE_ERR_NOMEM;
     c->device = dev;
     c->num_sms = sms;
     c->wait_limit_ns = 2000000000ull;
+    memset(c->clusters, 0, sizeof c->clusters);
+    if (fp8_gemm_setup(c->clusters) != cudaSuccess) {
+        delete c;
+        return MOE_ERR_CUDA;
+    }
     if (cudaMalloc(&c->err, 64) != cudaSuccess) {
         cudaGetLastError();
         delete c;
@@ -258,7 +266,7 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
     if (!g.ok) return MOE_ERR_CUDA;
     if (fp8_few(M, F, 1, c->num_sms)) {
         Fp8FewParams p = few_params(M, F, K, a, lda, a_scale, w13, w13_scale, b13);
-        p.alpha = alpha;
+        p.minus_alpha_log2e = -1.44269504f * alpha;
         p.limit = limit;
         p.shift = shift;
         p.h = h;
@@ -268,7 +276,7 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
     Fp8GemmParams p;
     Fp8Plan pl;
     if ((rc = product_params(c, p, pl, 1, M, F, K, a, lda, a_scale, w13, w13_scale, b13))) return rc;
-    p.alpha = alpha;
+    p.minus_alpha_log2e = -1.44269504f * alpha;
     p.limit = limit;
     p.shift = shift;
     p.h = h;
@@ -277,12 +285,15 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
 }
 
 int moe_fp8_debug_plan(int gated, int M, int N, int K, int num_sms, int *out) {
-    if (!out || M < 1 || N < 1 || K < 16 || K % 16 || num_sms < 1 || (gated && N % 16)) return MOE_ERR_ARG;
+    if (!out || M < 1 || N < 1 || K < 16 || K % 16 || num_sms < 1 || (gated && N % 16) || N > FP8_SIZE_MAX)
+        return MOE_ERR_ARG;
     Fp8Plan pl;
-    if (!fp8_plan(M, N, K, gated ? 1 : 0, num_sms, &pl)) return MOE_ERR_ARG;
-    const int v[] = {pl.bn, pl.ctas, pl.cl, pl.a_rows, pl.n_stages, pl.m_tiles, pl.tiles, pl.grid, pl.smem,
-                     fp8_smem(pl.bn, pl.ctas, pl.cl, gated ? 1 : 0, pl.a_rows, pl.n_stages).total, pl.tmem_cols,
-                     fp8_ctas_per_sm(pl.bn)};
+    int clusters[FP8_SPLIT_MAX + 1];
+    for (int n = 1; n <= FP8_SPLIT_MAX; ++n) clusters[n] = num_sms / n;
+    const int few = fp8_few(M, N, gated ? 1 : 0, num_sms) ? 1 : 0;
+    if (!fp8_plan(M, N, K, gated ? 1 : 0, num_sms, clusters, &pl)) return MOE_ERR_ARG;
+    const int v[] = {few, pl.bn, pl.ctas, pl.split, pl.a_rows, pl.n_stages, pl.m_tiles, pl.tiles, pl.grid,
+                     fp8_smem(pl.bn, pl.ctas, gated ? 1 : 0, pl.split > 1 || (gated && pl.ctas == 1), pl.a_rows, pl.n_stages).total};
     memcpy(out, v, sizeof v);
     return MOE_OK;
 }

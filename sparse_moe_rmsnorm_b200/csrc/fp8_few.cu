@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, few_ctas(GATED)) fp8_few_kerne
     } else {
         constexpr int PASSES = (TOK * FEW_ROWS + FEW_WARPS * 32 - 1) / (FEW_WARPS * 32);
         const uint32_t rank = cluster_ctarank();
-        const float minus_alpha_log2e = -1.44269504f * p.alpha;
         float hv[PASSES];
         cluster_wait();                             // every CTA of the cluster runs
 #pragma unroll
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32, few_ctas(GATED)) fp8_few_kerne
                 }
                 gt = fmin_nan(gt, p.limit);
                 u = fmax_nan(fmin_nan(u, p.limit), -p.limit);
-                hv[i] = gt * rcp_approx(1.0f + exp2_approx(minus_alpha_log2e * gt)) * (u + p.shift);
+                hv[i] = gt * rcp_approx(1.0f + exp2_approx(p.minus_alpha_log2e * gt)) * (u + p.shift);
                 amax = fabsf(hv[i]);
             }
             // over the 16 columns (neighbouring lanes), then to every CTA of the cluster

@@ -14,14 +14,21 @@
 // gate rows and half linear rows of W13, so a thread holds a row's gate and linear value of the
 // same columns, computes h = min(g, L) sigmoid(alpha min(g, L)) (clamp(u, -L, L) + shift), and
 // writes h in E4M3 with the scale of its 128-column block; only the block's maximum crosses
-// warps (or, for narrow tiles, the CTAs of a cluster, through distributed shared memory).
+// warps.
 //
-// Warp roles: 4 or 8 epilogue warps (warp w reads TMEM lane quarter w % 4), then the TMA
-// producer, then two MMA warps, one elected lane of each running its loop, then
-// the warp that fetches the scales (16 K blocks ahead: loads of them in the epilogue's loop put a
-// round trip to L2 on every block).
-// Persistent: CTAs (clusters) walk the output tiles, rows fastest, so the B tile of neighbouring
-// CTAs is the same and A stays in L2.
+// Three forms (fp8_plan chooses):
+//   pairs   many tiles: two CTAs of a cluster share MMAs of 256 rows x 256 columns (cta_group::2), each
+//           holding its 128 rows' sums and half of B.  Persistent; a K block's accumulator is two
+//           parts of 128 columns, one per epilogue warpgroup, each filled and freed by itself.
+//   single  128 x 128 tiles, one CTA each, persistent: up to 128 rows by many columns.
+//   split   few tiles: the CTAs of a cluster split K (a block costs a CTA some 0.2 us of hand-overs whatever
+//           its size, so the chain of blocks is what takes the time), then join their sums through
+//           distributed shared memory, in a fixed order, each finishing some of the rows.
+//
+// Warp roles: 8 epilogue warps (warp w reads TMEM lane quarter w % 4), the TMA producer, two MMA
+// warps, one elected lane of each running its loop, then the warp that fetches the scales (16 K
+// blocks ahead: loads of them in the epilogue's loop put a round trip to L2 on every block).
+// Tiles are walked rows fastest, so the B tile of neighbouring CTAs is the same and A stays in L2.
 //
 // Every wait is bounded (WaitCtl); when one runs out the CTA stops issuing, waits (bounded) for
 // what it has in flight, frees TMEM and returns with the error latched.
@@ -41,6 +48,13 @@ namespace {
 constexpr unsigned int FP8_ERR_WAIT = 1u;
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
+
+// h of a gate and a linear value: min(g, L) sigmoid(alpha min(g, L)) (clamp(u, -L, L) + shift).
+__device__ __forceinline__ float gated_value(const Fp8GemmParams &p, float g, float u) {
+    g = fmin_nan(g, p.limit);
+    u = fmax_nan(fmin_nan(u, p.limit), -p.limit);
+    return g * rcp_approx(1.0f + exp2_approx(p.minus_alpha_log2e * g)) * (u + p.shift);
+}
 
 // V elements (1 or 4) of type T.
 template <typename T, int V>
@@ -139,12 +153,98 @@ __device__ __forceinline__ void store_columns(const Fp8GemmParams &p, const floa
                         make_float4(acc[s * CC + i], acc[s * CC + i + 1], acc[s * CC + i + 2], acc[s * CC + i + 3]);
                 b = bias[s * CC / 32];
             }
-        if (CC < 32) b = __shfl_sync(0xffffffffu, b, (part * CC + lane) % 32);     // this part's columns from lane 0 on
         __syncwarp();
         if (p.type == FP8_BF16) put_tile<__nv_bfloat16, CC>(p, tile, b, m0, n0 + part * CC, lane);
         else if (p.type == FP8_FP16) put_tile<__half, CC>(p, tile, b, m0, n0 + part * CC, lane);
         else put_tile<float, CC>(p, tile, b, m0, n0 + part * CC, lane);
         __syncwarp();
+    }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// The sum over the cluster's CTAs, in their order, of four neighbouring sums at byte `at` of their tiles.
+__device__ __forceinline__ float4 parts_sum(uint32_t tile, uint32_t at, int split) {
+    float4 v[FP8_SPLIT_MAX];
+#pragma unroll
+    for (int c = 0; c < FP8_SPLIT_MAX; ++c)
+        if (c < split) v[c] = ld_cluster_f32x4(map_to_rank(tile + at, (uint32_t)c));
+    float4 t = v[0];
+#pragma unroll
+    for (int c = 1; c < FP8_SPLIT_MAX; ++c)
+        if (c < split) t.x += v[c].x, t.y += v[c].y, t.z += v[c].z, t.w += v[c].w;
+    return t;
+}
+
+template <typename T>
+__device__ __forceinline__ void put_four(const Fp8GemmParams &p, long long row, int n, float (&o)[4]) {
+    T *c = static_cast<T *>(p.c) + row * p.ldc + n;
+    const T *res = static_cast<const T *>(p.residual);
+    if (res) res += row * p.ldr + n;
+    if (p.vec && n + 4 <= p.N) {
+        Pack<T, 4> v;
+        if (res) {
+            v.raw = *reinterpret_cast<const decltype(v.raw) *>(res);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] += v.get(j);
+        }
+        v.set(o);
+        *reinterpret_cast<decltype(v.raw) *>(c) = v.raw;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < p.N) c[j] = static_cast<T>(res ? o[j] + static_cast<float>(res[j]) : o[j]);
+    }
+}
+
+// A tile whose K the cluster's CTAs have split: every CTA finishes some of the rows, a warp a row, a lane four
+// columns (gated: four columns of h), reading all CTAs' sums through distributed shared memory.
+template <int BN, bool GATED>
+__device__ __forceinline__ void join_parts(const Fp8GemmParams &p, uint32_t tile, int rank, int t, int warp, int lane) {
+    const int nt = t / p.m_tiles, m0 = (t - nt * p.m_tiles) * FP8_BM;
+    const int rows = min(FP8_BM, p.M - m0), each = (rows + p.split - 1) / p.split;
+    const int n = nt * 128 + 4 * lane;          // BN columns of c, or BN / 2 of h: 128
+    float b[2][4];
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[h][j] = p.bias && n + j < p.N ? bf16_bits_to_f32(p.bias[h * p.N + n + j]) : 0.0f;
+#pragma unroll 1
+    for (int r = rank * each + warp; r < min(rows, (rank + 1) * each); r += FP8_WGS * 4) {
+        const uint32_t row = (uint32_t)(r * (BN + 4)) * 4;
+        const long long m = m0 + r;
+        if constexpr (!GATED) {
+            const float4 v = parts_sum(tile, row + 16 * lane, p.split);
+            if (n >= p.N) continue;
+            float o[4] = {v.x + b[0][0], v.y + b[0][1], v.z + b[0][2], v.w + b[0][3]};
+            if (p.type == FP8_BF16) put_four<__nv_bfloat16>(p, m, n, o);
+            else if (p.type == FP8_FP16) put_four<__half>(p, m, n, o);
+            else put_four<float>(p, m, n, o);
+        } else {
+            // a warpgroup's columns are 64 gate and 64 linear ones
+            const uint32_t at = row + (uint32_t)(lane / 16 * 128 + lane % 16 * 4) * 4;
+            const float4 gv = parts_sum(tile, at, p.split), uv = parts_sum(tile, at + 256, p.split);
+            const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
+            float h[4], amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = gated_value(p, gs[j] + b[0][j], us[j] + b[1][j]);
+                if (n + j < p.N) amax = fmax_nan(amax, fabsf(h[j]));
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) amax = fmax_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float s = fmax_nan(amax / FP8_MAX, FP8_SCALE_MIN), inv = 1.0f / s;
+            if (n < p.N)                        // F is a multiple of 16
+                *reinterpret_cast<uint32_t *>(p.h + m * p.N + n) = f32x4_to_e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+            if (lane == 0) p.h_scale[m * p.NB + nt] = s;
+        }
     }
 }
 
@@ -158,24 +258,23 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity, unsig
 
 }  // namespace
 
-template <int BN, int CTAS, bool GATED, int CL>
-__global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
-    constexpr int WGS = fp8_wgs(BN);            // epilogue warpgroups
+template <int BN, int CTAS, bool GATED, bool SK>
+__global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
+    constexpr int WGS = FP8_WGS;                // epilogue warpgroups
     constexpr int CW = BN / WGS;                // accumulator columns per epilogue thread
     constexpr int LD = 16;                      // columns of a TMEM load (registers: 2 LD beside the CW sums)
-    constexpr int CC = fp8_tile_cols(BN);       // columns of a staging tile
+    constexpr int CC = FP8_TILE_COLS;           // columns of a staging tile
     constexpr int HW = CW / 2;                  // gated: h columns per thread
     constexpr int BUFS = fp8_bufs(BN);
     constexpr int SPLIT = fp8_split(BN);        // parts of an accumulator: one per warpgroup, or the whole
     constexpr int PN = BN / SPLIT;              // columns of an MMA
-    constexpr int CSIZE = CTAS == 2 ? 2 : CL;   // CTAs per cluster
-    constexpr int EX = WGS > CL ? WGS : CL;     // gated: warps or CTAs that share a row's block
-    static_assert(BUFS % 2 == 0, "with an accumulator's uses, too, one MMA warp's");
-    static_assert(!GATED || HW * EX == FP8_BLOCK, "a gated row's block is shared by EX threads");
+    static_assert(BUFS % 2 == 0, "an accumulator's uses are one MMA warp's, too");
+    static_assert(!GATED || HW * WGS == FP8_BLOCK, "the warpgroups share a gated row's block");
+    static_assert(!SK || CTAS == 1, "CTAs of a cluster split K, or are a pair");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int NS = p.n_stages;
-    const Fp8Smem plan = fp8_smem(BN, CTAS, CL, GATED, p.a_rows, NS);
+    const Fp8Smem plan = fp8_smem(BN, CTAS, GATED, SK, p.a_rows, NS);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + plan.bar_off);
     uint64_t *empty = full + NS;
     uint64_t *d_full = empty + NS;              // [SPLIT][BUFS] a K block's accumulator (part) is complete
@@ -185,12 +284,12 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
     uint64_t *sc_full = ex_bar + 8;             // [FP8_CHUNKS] a chunk of scales is there
     uint64_t *sc_empty = sc_full + FP8_CHUNKS;  // ... and has been read
     const uint32_t scales0 = smem_addr(smem + plan.scale_off);
-    float *ex = reinterpret_cast<float *>(smem + plan.ex_off);       // [2 parities][EX][128 rows]
+    float *ex = reinterpret_cast<float *>(smem + plan.ex_off);       // [2 parities][2 warpgroups][128 rows]
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(smem + plan.misc_off);
     volatile int *abort_s = reinterpret_cast<volatile int *>(smem + plan.misc_off + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CSIZE > 1 ? cluster_ctarank() : 0;
+    const uint32_t rank = CTAS > 1 || SK ? cluster_ctarank() : 0;
     constexpr int TMA_WARP = WGS * 4, MMA_WARP = TMA_WARP + 1, SCALE_WARP = TMA_WARP + 3;
     constexpr uint32_t COLS = BUFS * BN;
 
@@ -205,7 +304,7 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
         }
         mbar_init(&drain_bar[0], 1);
         mbar_init(&drain_bar[1], 1);
-        for (int i = 0; i < 8; ++i) mbar_init(&ex_bar[i], EX);
+        for (int i = 0; i < 8; ++i) mbar_init(&ex_bar[i], WGS);
         for (int i = 0; i < FP8_CHUNKS; ++i) {
             mbar_init(&sc_full[i], 32);         // every lane of the scale warp
             mbar_init(&sc_empty[i], WGS * 4);   // every epilogue warp
@@ -216,25 +315,28 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
     if (warp == MMA_WARP) tmem_alloc_g<CTAS>(tmem_base_s, COLS);
     tc_fence_before();
     __syncthreads();
-    if constexpr (CSIZE > 1) cluster_sync();    // the peers' barriers are initialised
+    if constexpr (CTAS > 1) cluster_sync();     // the peer's barriers are initialised
     tc_fence_after();
     pdl_wait();
     pdl_trigger();
     const uint32_t tmem = *tmem_base_s;
     const WaitCtl wc{abort_s, p.err, FP8_ERR_WAIT, p.wait_limit_ns};
-    const int first = blockIdx.x / CSIZE, step = gridDim.x / CSIZE;
+    // SK: a cluster takes one tile, each of its CTAs a part of K
+    const int group = SK ? p.split : CTAS;
+    const int first = blockIdx.x / group, step = gridDim.x / group;
+    const int kb0 = SK ? p.KB * (int)rank / p.split : 0, kb1 = SK ? p.KB * ((int)rank + 1) / p.split : p.KB;
 
-    // Register shares of the wide variants (3 warpgroups of 168 at launch): 224 for the two that hold
+    // Register shares (3 warpgroups of 168 at launch): 224 for the two that hold
     // the sums, 56 for the producers', 2 x 224 + 56 = 3 x 168.
     if (warp >= WGS * 4) {
-        if constexpr (WGS > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == TMA_WARP && elect_one()) {
             tma_prefetch_desc(&p.map_a);
             tma_prefetch_desc(&p.map_b);
             const uint32_t a0 = smem_addr(smem), b0 = smem_addr(smem + plan.b_off), full0 = smem_addr(full), empty0 = smem_addr(empty);
             const uint32_t a_stage = plan.a_stage, b_stage = plan.b_stage;
             const uint32_t bytes = CTAS * (a_stage + b_stage);
-            const int KB = p.KB, tiles = p.tiles, m_tiles = p.m_tiles;
+            const int tiles = p.tiles, m_tiles = p.m_tiles;
             int slot = 0;
             uint32_t ph = 0, fills = 0;                 // fills: at most NS are of interest
             bool ok = true;
@@ -242,8 +344,8 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                 const int nt = t / m_tiles;
                 const int m0 = (t - nt * m_tiles) * (FP8_BM * CTAS) + (CTAS == 2 ? (int)rank * FP8_BM : 0);
                 // B rows: of a pair, each CTA brings half of each part's columns (gated: the gate rows or the linear ones)
-                const int nb = GATED ? nt * FP8_BLOCK + (CTAS == 2 ? 0 : (int)rank * HW) : nt * BN + (CTAS == 2 ? (int)rank * (PN / 2) : 0);
-                for (int kb = 0, k0 = 0; kb < KB; ++kb, k0 += FP8_KS) {
+                const int nb = GATED ? nt * FP8_BLOCK : nt * BN + (CTAS == 2 ? (int)rank * (PN / 2) : 0);
+                for (int kb = kb0, k0 = kb0 * FP8_KS; kb < kb1; ++kb, k0 += FP8_KS) {
                     const uint32_t bar = full0 + 8u * slot;
                     if (!wait_phase<false>(empty0 + 8u * slot, ph ^ 1, wc)) { ok = false; break; }
                     if (CTAS == 1 || rank == 0) mbar_arrive_expect_tx(bar, bytes);
@@ -254,8 +356,11 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                         for (int h = 0; h < SPLIT; ++h)
                             tma_load_3d<2>(bs + h * (PN / 2) * FP8_KS, &p.map_b, bar, k0, nb + h * (GATED ? HW : PN), GATED ? (int)rank : 0);
                     } else {
-                        tma_load_3d<1>(bs, &p.map_b, bar, k0, nb, 0);
-                        if constexpr (GATED) tma_load_3d<1>(bs + HW * FP8_KS, &p.map_b, bar, k0, nb, 1);
+#pragma unroll
+                        for (int h = 0; h < SPLIT; ++h) {
+                            tma_load_3d<1>(bs + h * PN * FP8_KS, &p.map_b, bar, k0, nb + h * (GATED ? HW : PN), 0);
+                            if constexpr (GATED) tma_load_3d<1>(bs + (h * PN + HW) * FP8_KS, &p.map_b, bar, k0, nb + h * HW, 1);
+                        }
                     }
                     fills = min(fills + 1, (uint32_t)NS);
                     if (++slot == NS) { slot = 0; ph ^= 1; }
@@ -276,7 +381,7 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
             constexpr int BY = SPLIT == 2 ? 1 : 2;              // blocks between two of this warp's
             const int m = warp - MMA_WARP, part = SPLIT == 2 ? m : 0;
             const int skip = SPLIT == 2 ? 0 : m;
-            const long long blocks = (long long)((p.tiles - first + step - 1) / step) * p.KB;
+            const long long blocks = (long long)((p.tiles - first + step - 1) / step) * (kb1 - kb0);
             const uint32_t full0 = smem_addr(full), empty0 = smem_addr(empty);
             const uint32_t d_full0 = smem_addr(d_full + part * BUFS), d_empty0 = smem_addr(d_empty + part * BUFS);
             const uint64_t ad0 = smem_desc_sw128(smem_addr(smem));
@@ -325,10 +430,10 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                 const int blk = (GATED ? nt * FP8_BLOCK : nt * BN + r0 * CW) / FP8_BLOCK;
                 const bool has_b = r0 < (GATED ? 2 : WGS) && blk < p.NB;
                 const float *sb = p.b_scale + ((long long)(GATED ? r0 * p.NB : 0) + blk) * p.KB + k;
-                for (int kb = 0; kb < p.KB; kb += FP8_CHUNK) {
+                for (int kb = kb0; kb < kb1; kb += FP8_CHUNK) {
                     if (!__all_sync(0xffffffffu, wait_phase<false>(empty0 + 8u * cb, ph ^ 1, wc))) { ok = false; break; }
                     const uint32_t dst = dst0 + (uint32_t)(cb * FP8_CHUNK_BYTES);
-                    if (kb + k < p.KB) {
+                    if (kb + k < kb1) {
                         const float *src = sa + kb;
 #pragma unroll
                         for (int i = 0; i < FP8_BM / RPI; ++i, src += next)
@@ -341,18 +446,20 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
             }
             cp_async_wait_all();
         }
+        __syncwarp();
+        if constexpr (SK) cluster_sync();       // (with the epilogue warps' below)
     } else {
-        if constexpr (WGS > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int wg = warp >> 2, q = warp & 3;
         const int part = SPLIT == 2 ? wg : 0;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(SPLIT == 2 ? wg * BUFS * PN : wg * CW);
         const uint32_t d_full0 = smem_addr(d_full + part * BUFS);
-        const uint32_t d_empty0 = CTAS == 2 ? map_to_rank(smem_addr(d_empty + part * BUFS), 0) : smem_addr(d_empty);
+        const uint32_t d_empty_here = smem_addr(d_empty + part * BUFS);
+        const uint32_t d_empty0 = CTAS == 2 ? map_to_rank(d_empty_here, 0) : d_empty_here;
         const uint32_t sc_full0 = smem_addr(sc_full), sc_empty0 = smem_addr(sc_empty);
         int buf = 0, par = 0, cb = 0;
         uint32_t dph = 0, exph = 0, cph = 0;
         bool ok = true;
-        const int KB = p.KB;
         auto release = [&](uint32_t bar) {          // the warp has read its columns of an accumulator
             tc_fence_before();
             __syncwarp();
@@ -365,7 +472,7 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
             // first row and column of the warp's part of the tile
             const int nt = t / p.m_tiles;
             const int m0 = (t - nt * p.m_tiles) * (FP8_BM * CTAS) + (CTAS == 2 ? (int)rank * FP8_BM : 0) + 32 * q;
-            const int n0 = GATED ? nt * FP8_BLOCK + (WGS > 1 ? wg : (int)rank) * HW : nt * BN + wg * CW;
+            const int n0 = GATED ? nt * FP8_BLOCK + wg * HW : nt * BN + wg * CW;
             const bool active = m0 < p.M && n0 < p.N;      // the warp has something to write
             // lane i: the biases of the columns 32 j + i (gated: of the gate, then of the linear part), read
             // here so that they have arrived when the sums are complete
@@ -373,16 +480,16 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
 #pragma unroll
             for (int j = 0; j < (CW + 31) / 32; ++j) {
                 const int i = 32 * j + lane, col = n0 + (GATED ? i % HW : i);
-                bias[j] = p.bias && i < CW && col < p.N ? bf16_bits_to_f32(p.bias[(GATED && i >= HW ? p.N : 0) + col]) : 0.0f;
+                bias[j] = !SK && p.bias && col < p.N ? bf16_bits_to_f32(p.bias[(GATED && i >= HW ? p.N : 0) + col]) : 0.0f;
             }
             float acc[CW];
 #pragma unroll
             for (int i = 0; i < CW; ++i) acc[i] = 0.0f;
-            for (int kb = 0; kb < KB; kb += FP8_CHUNK) {
+            for (int kb = kb0; kb < kb1; kb += FP8_CHUNK) {
                 wait_phase_through(sc_full0 + 8u * cb, cph, wc);
                 const float *sc = reinterpret_cast<const float *>(smem + plan.scale_off + cb * FP8_CHUNK_BYTES);
                 const float *sa = sc + (32 * q + lane) * FP8_CHUNK, *sb = sc + (FP8_BM + (GATED ? 0 : wg)) * FP8_CHUNK;
-                const int blocks = min(FP8_CHUNK, KB - kb);
+                const int blocks = min(FP8_CHUNK, kb1 - kb);
 #pragma unroll 1
                 for (int k = 0; k < blocks; ++k) {
                     const float s0 = sa[k] * sb[k], s1 = GATED ? sa[k] * sb[FP8_CHUNK + k] : 0.0f;
@@ -413,42 +520,41 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                 if (++cb == FP8_CHUNKS) { cb = 0; cph ^= 1; }
                 if (__any_sync(0xffffffffu, *abort_s)) { ok = false; break; }
             }
-            if (!ok) break;
-            if constexpr (GATED) {
+            if constexpr (SK) {
+                // every warpgroup's last block is complete, so no copy or MMA uses the rings: the sums go there
+                asm volatile("bar.sync 1, %0;" ::"n"(WGS * 128) : "memory");
                 const int row = 32 * q + lane;
-                const float minus_alpha_log2e = -1.44269504f * p.alpha;
-                float amax = 0.0f, h[HW];
-                const float *bs = reinterpret_cast<const float *>(smem + plan.stage_off + warp * fp8_tile_bytes(BN, 1));
+                if (row < p.a_rows) {
+                    float *to = reinterpret_cast<float *>(smem) + row * (BN + 4) + wg * CW;
 #pragma unroll
-                for (int j = 0; j < (CW + 31) / 32; ++j)
-                    if (32 * j + lane < CW) const_cast<float *>(bs)[32 * j + lane] = bias[j];
+                    for (int i = 0; i < CW; i += 4)
+                        *reinterpret_cast<float4 *>(to + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                }
+                break;
+            }
+            if (!ok) break;
+            if constexpr (GATED && !SK) {
+                const int row = 32 * q + lane;
+                float amax = 0.0f, h[HW];
+                float *bs = reinterpret_cast<float *>(smem + plan.stage_off + warp * fp8_tile_bytes(1));
+#pragma unroll
+                for (int j = 0; j < (CW + 31) / 32; ++j) bs[32 * j + lane] = bias[j];
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < HW; ++i) {
-                    const float g = fmin_nan(acc[i] + bs[i], p.limit);
-                    const float u = fmax_nan(fmin_nan(acc[HW + i] + bs[HW + i], p.limit), -p.limit);
-                    h[i] = g * rcp_approx(1.0f + exp2_approx(minus_alpha_log2e * g)) * (u + p.shift);
+                    h[i] = gated_value(p, acc[i] + bs[i], acc[HW + i] + bs[HW + i]);
                     if (n0 + i < p.N) amax = fmax_nan(amax, fabsf(h[i]));
                 }
                 __syncwarp();
                 // the row's maximum over its 128-column block
-                float *slot = ex + (par * EX) * FP8_BM + row;
+                float *slot = ex + par * WGS * FP8_BM + row;
                 uint64_t *bar = &ex_bar[2 * q + par];
-                if constexpr (CL > 1) {
+                slot[wg * FP8_BM] = amax;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+                if (!__all_sync(0xffffffffu, wait_phase<false>(smem_addr(bar), exph, wc))) { ok = false; break; }
 #pragma unroll
-                    for (int c = 0; c < CL; ++c)
-                        st_cluster_f32(map_to_rank(smem_addr(slot + rank * FP8_BM), (uint32_t)c), amax);
-                    __syncwarp();
-                    if (lane < CL) mbar_arrive_cluster(map_to_rank(smem_addr(bar), (uint32_t)lane));
-                    if (!__all_sync(0xffffffffu, wait_phase<true>(smem_addr(bar), exph, wc))) { ok = false; break; }
-                } else {
-                    slot[wg * FP8_BM] = amax;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
-                    if (!__all_sync(0xffffffffu, wait_phase<false>(smem_addr(bar), exph, wc))) { ok = false; break; }
-                }
-#pragma unroll
-                for (int e = 0; e < EX; ++e) amax = fmax_nan(amax, slot[e * FP8_BM]);
+                for (int e = 0; e < WGS; ++e) amax = fmax_nan(amax, slot[e * FP8_BM]);
                 par ^= 1;
                 if (par == 0) exph ^= 1;
                 if (active && m0 + lane < p.M) {
@@ -467,66 +573,75 @@ __global__ void __launch_bounds__(fp8_threads(BN), fp8_ctas_per_sm(BN)) fp8_gemm
                         }
                     if (n0 % FP8_BLOCK == 0) p.h_scale[(long long)(m0 + lane) * p.NB + n0 / FP8_BLOCK] = s;
                 }
-            } else if (active) {
-                store_columns<CW, CC>(p, acc, bias, reinterpret_cast<float *>(smem + plan.stage_off + warp * fp8_tile_bytes(BN, 0)), m0, n0, lane);
+            } else if (!SK && active) {
+                store_columns<CW, CC>(p, acc, bias, reinterpret_cast<float *>(smem + plan.stage_off + warp * fp8_tile_bytes(0)), m0, n0, lane);
             }
+        }
+        if constexpr (SK) {
+            cluster_sync();                     // every CTA's sums are in its shared memory
+            join_parts<BN, GATED>(p, smem_addr(smem), (int)rank, first, warp, lane);
         }
     }
 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if constexpr (CSIZE > 1) cluster_sync();    // no CTA leaves while a peer may still reach its shared memory
+    if constexpr (CTAS > 1 || SK) cluster_sync();   // no CTA leaves while a peer may still reach its shared memory
     tc_fence_after();
     if (warp == MMA_WARP) tmem_dealloc_g<CTAS>(tmem, COLS);
 }
 
-template <int BN, int CTAS, bool GATED, int CL>
+template <int BN, int CTAS, bool GATED, bool SK>
 static cudaError_t launch_t(const Fp8GemmParams &p, const Fp8Plan &pl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.grid);
-    cfg.blockDim = dim3(fp8_threads(BN));
-    cfg.dynamicSmemBytes = pl.smem;
+    cfg.blockDim = dim3(FP8_THREADS);
+    cfg.dynamicSmemBytes = FP8_SMEM_SM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CTAS == 2 ? 2 : CL;
+    attr[1].val.clusterDim.x = SK ? pl.split : CTAS;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CTAS == 2 || CL > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN, CTAS, GATED, CL>, p);
+    cfg.numAttrs = CTAS == 2 || SK ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN, CTAS, GATED, SK>, p);
 }
 
-template <int BN, int CTAS, bool GATED, int CL>
+template <int BN, int CTAS, bool GATED, bool SK>
 static cudaError_t setup_t() {
-    return cudaFuncSetAttribute(fp8_gemm_kernel<BN, CTAS, GATED, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                fp8_smem_bytes(BN));
+    return cudaFuncSetAttribute(fp8_gemm_kernel<BN, CTAS, GATED, SK>, cudaFuncAttributeMaxDynamicSharedMemorySize, FP8_SMEM_SM);
 }
 
-// Once per device, before the first launch.
-cudaError_t fp8_gemm_setup() {
-    cudaError_t e = setup_t<32, 1, false, 1>();
-    if (e == cudaSuccess) e = setup_t<64, 1, false, 1>();
-    if (e == cudaSuccess) e = setup_t<128, 1, false, 1>();
-    if (e == cudaSuccess) e = setup_t<32, 1, true, 8>();
-    if (e == cudaSuccess) e = setup_t<64, 1, true, 4>();
-    if (e == cudaSuccess) e = setup_t<256, 2, false, 1>();
-    if (e == cudaSuccess) e = setup_t<256, 2, true, 1>();
+// Once per device, before the first launch: the kernels' shared memory, and how many clusters of 1 to
+// FP8_SPLIT_MAX CTAs the device holds at once (an SM to a CTA; a cluster lies in one GPC).
+cudaError_t fp8_gemm_setup(int *clusters) {
+    cudaError_t e = setup_t<128, 1, false, false>();
+    if (e == cudaSuccess) e = setup_t<128, 1, false, true>();
+    if (e == cudaSuccess) e = setup_t<256, 1, true, true>();
+    if (e == cudaSuccess) e = setup_t<256, 2, false, false>();
+    if (e == cudaSuccess) e = setup_t<256, 2, true, false>();
+    for (int n = 1; n <= FP8_SPLIT_MAX && e == cudaSuccess; ++n) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n);
+        cfg.blockDim = dim3(FP8_THREADS);
+        cfg.dynamicSmemBytes = FP8_SMEM_SM;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = n;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&clusters[n], fp8_gemm_kernel<128, 1, false, true>, &cfg);
+    }
     return e;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s) {
-    if (gated) {
-        if (pl.bn == 256) return launch_t<256, 2, true, 1>(p, pl, s);
-        if (pl.bn == 32) return launch_t<32, 1, true, 8>(p, pl, s);
-        return launch_t<64, 1, true, 4>(p, pl, s);
-    }
-    if (pl.bn == 256) return launch_t<256, 2, false, 1>(p, pl, s);
-    if (pl.bn == 32) return launch_t<32, 1, false, 1>(p, pl, s);
-    if (pl.bn == 64) return launch_t<64, 1, false, 1>(p, pl, s);
-    return launch_t<128, 1, false, 1>(p, pl, s);
+    if (gated) return pl.ctas == 2 ? launch_t<256, 2, true, false>(p, pl, s) : launch_t<256, 1, true, true>(p, pl, s);
+    if (pl.ctas == 2) return launch_t<256, 2, false, false>(p, pl, s);
+    return pl.split > 1 ? launch_t<128, 1, false, true>(p, pl, s) : launch_t<128, 1, false, false>(p, pl, s);
 }
 
 }  // namespace moe

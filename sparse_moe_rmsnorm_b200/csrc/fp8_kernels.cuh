@@ -34,13 +34,14 @@ struct Fp8GemmParams {
     int M, N, K, KB, NB;            // N: output columns (gated: F)
     int m_tiles, tiles;
     int a_rows, n_stages;           // rows of an A stage (128, or M rounded up to 8 below that)
+    int split;                      // CTAs of a cluster that share a tile's K
     const uint16_t *bias;           // bf16 [N] (gated [2 F]) or NULL
     const void *residual;           // type [M, N], rows ldr elements apart, or NULL
     void *c;                        // type [M, N], rows ldc elements apart
     long long ldr, ldc;
     int type;                       // FP8_BF16, FP8_FP16 or FP8_FP32
     int vec;                        // four elements of a row of c (and of the residual) move as one
-    float alpha, limit, shift;      // gated activation
+    float minus_alpha_log2e, limit, shift;      // gated activation
     uint8_t *h;                     // gated: E4M3 [M, F]
     float *h_scale;                 // gated: [M, NB]
     unsigned int *err;
@@ -64,107 +65,109 @@ struct Fp8FewParams {
     float *h_scale;
     long long lda, ldr, ldc;
     int M, N, K, KB, NB, type;
-    float alpha, limit, shift;
+    float minus_alpha_log2e, limit, shift;
 };
 
-// One kernel variant: BN columns of accumulators per CTA (gated: BN / 2 gate and BN / 2 linear
-// columns), CTAS CTAs per MMA, CL CTAs of a cluster sharing a gated row's 128-column block.
+// One launch: BN columns of accumulators per CTA (gated: BN / 2 gate and BN / 2 linear columns), CTAS CTAs
+// per MMA, K split over `split` CTAs of a cluster.
 struct Fp8Plan {
-    int bn, ctas, cl;
+    int bn, ctas, split;
     int a_rows, n_stages;
-    int m_tiles, tiles, grid, smem, tmem_cols;
+    int m_tiles, tiles, grid;
 };
 
+constexpr int FP8_SIZE_MAX = 1 << 30;   // rows, columns and K, at most
 constexpr int FP8_BM = 128;             // rows of A per CTA (TMEM lanes)
 constexpr int FP8_KS = 128;             // K elements per stage: one scale block
 constexpr int FP8_STAGES_MAX = 16;
-constexpr int FP8_SMEM_SM = 227 * 1024; // shared memory of a CTA that has its SM alone
-// ... and of one of two CTAs on an SM: an SM's 228 KB hold two of these and the 1 KB that each reserves.
-constexpr int FP8_SMEM_HALF = 113 * 1024;
+constexpr int FP8_SPLIT_MAX = 8;        // CTAs of a cluster
+constexpr int FP8_WGS = 2;              // epilogue warpgroups
+constexpr int FP8_THREADS = FP8_WGS * 128 + 128;
+// A CTA has its SM alone, with all of its tensor memory: whatever its rings need, it takes all of the shared
+// memory, so no other of these CTAs (nor the expert GEMM's) can lie beside it and wait for TMEM columns
+// while a peer in its cluster waits for it.
+constexpr int FP8_SMEM_SM = 227 * 1024;
+constexpr int FP8_TMEM_COLS = 512;
 
-__host__ __device__ constexpr int fp8_wgs(int bn) { return bn >= 128 ? 2 : 1; }      // epilogue warpgroups
-__host__ __device__ constexpr int fp8_bufs(int bn) { return bn == 256 ? 2 : bn == 32 ? 8 : 4; }   // accumulators of BN columns
-__host__ __device__ constexpr int fp8_split(int bn) { return bn == 256 ? 2 : 1; }   // parts that an accumulator fills and frees in
-// A variant takes its share of an SM's shared memory as it takes TMEM (512 or 256 of the 512
-// columns), whatever its rings need: CTAs that fit an SM together then find their TMEM columns
-// free, so no allocation waits while a CTA of the same cluster waits for it.
-__host__ __device__ constexpr int fp8_ctas_per_sm(int bn) { return fp8_bufs(bn) * bn == 512 ? 1 : 2; }
-__host__ __device__ constexpr int fp8_smem_bytes(int bn) { return fp8_ctas_per_sm(bn) == 1 ? FP8_SMEM_SM : FP8_SMEM_HALF; }
-__host__ __device__ constexpr int fp8_threads(int bn) { return fp8_wgs(bn) * 128 + 128; }
-
+__host__ __device__ constexpr int fp8_bufs(int bn) { return FP8_TMEM_COLS / bn; }       // accumulators of BN columns
+__host__ __device__ constexpr int fp8_split(int bn) { return bn == 256 ? 2 : 1; }       // parts that one fills and frees in
 // The scales on their way to the epilogue: a ring of chunks of four K blocks, in a chunk a row's four
 // scales side by side, for the CTA's 128 rows and two of the weight's blocks (each warpgroup's, or the
 // gate's and the linear part's).
 constexpr int FP8_CHUNK = 4, FP8_CHUNKS = 4;
 constexpr int FP8_CHUNK_BYTES = (FP8_BM + 2) * FP8_CHUNK * 4;
 constexpr int FP8_SCALE_BYTES = FP8_CHUNKS * FP8_CHUNK_BYTES;
-// An epilogue warp's staging tile: 32 rows of 32 or 16 sums, rows 16 bytes further apart than they are long
-// (gated: the biases of its columns).
-__host__ __device__ constexpr int fp8_tile_cols(int bn) { return fp8_wgs(bn) > 1 ? 32 : 16; }
-__host__ __device__ constexpr int fp8_tile_bytes(int bn, int gated) {
-    return gated ? bn / fp8_wgs(bn) * 4 : 32 * (fp8_tile_cols(bn) + 4) * 4;
-}
+// An epilogue warp's staging tile: 32 rows of 32 sums, rows 16 bytes further apart than they are long
+// (gated: the biases of its 128 columns).
+constexpr int FP8_TILE_COLS = 32;
+__host__ __device__ constexpr int fp8_tile_bytes(int gated) { return gated ? 128 * 4 : 32 * (FP8_TILE_COLS + 4) * 4; }     // (a split tile: none)
 
-// Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's staging
-// tile, the scales, the barriers, the row maxima that warps or CTAs exchange, the TMEM base and abort flag.
+// Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's staging tile, the
+// scales, the barriers, the row maxima that warps exchange, the TMEM base and abort flag.
 struct Fp8Smem {
     int a_stage, b_stage, b_off, stage_off, scale_off, bar_off, ex_off, misc_off, total;
 };
 
-__host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int cl, int gated, int a_rows, int n_stages) {
+__host__ __device__ inline Fp8Smem fp8_smem(int bn, int ctas, int gated, int split, int a_rows, int n_stages) {
     Fp8Smem s;
     s.a_stage = a_rows * FP8_KS;
     s.b_stage = bn / ctas * FP8_KS;
     s.b_off = n_stages * s.a_stage;
     s.stage_off = s.b_off + n_stages * s.b_stage;
-    s.scale_off = s.stage_off + fp8_wgs(bn) * 4 * fp8_tile_bytes(bn, gated);     // a multiple of 16
+    s.scale_off = s.stage_off + (split ? 0 : FP8_WGS * 4 * fp8_tile_bytes(gated));
     s.bar_off = s.scale_off + FP8_SCALE_BYTES;
     // full and empty per stage, full and empty per accumulator (part), drain [2 MMA warps], exchange
     // [4 quarters][2 parities], full and empty per chunk of scales
     s.ex_off = s.bar_off + (2 * n_stages + 2 * fp8_split(bn) * fp8_bufs(bn) + 2 + 8 + 2 * FP8_CHUNKS) * 8;
     s.ex_off = (s.ex_off + 15) / 16 * 16;
-    s.misc_off = s.ex_off + (gated ? 2 * (fp8_wgs(bn) > cl ? fp8_wgs(bn) : cl) * FP8_BM * 4 : 0);
+    s.misc_off = s.ex_off + (gated ? 2 * FP8_WGS * FP8_BM * 4 : 0);
     s.total = s.misc_off + 16;
-    // the MMA reads 128 rows of A from a stage's start, also where a stage holds fewer
-    const int a_end = (n_stages - 1) * s.a_stage + FP8_BM * FP8_KS;
+    // the MMA reads 128 rows of A from a stage's start, also where a stage holds fewer; a CTA that shares
+    // its tile's K puts its sums over the rings
+    const int a_end = (n_stages - 1) * s.a_stage + FP8_BM * FP8_KS, sums = split ? a_rows * (bn + 4) * 4 : 0;
     if (s.total < a_end) s.total = a_end;
+    if (s.total < sums) s.total = sums;
     s.total += 1024;
     return s;
 }
 
-// The variant, ring depth and grid of one product.  Returns false when the sizes are out of range.
-inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, Fp8Plan *pl) {
+// The form, ring depth and grid of one product; clusters[n]: how many clusters of n CTAs the device holds at
+// once.  Returns false when the sizes are out of range.
+inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, const int *clusters, Fp8Plan *pl) {
+    if (M > FP8_SIZE_MAX || N > FP8_SIZE_MAX || K > FP8_SIZE_MAX) return false;
     long long rows = (M + FP8_BM - 1) / FP8_BM;
-    auto cols = [&](int bn) -> long long { return gated ? fp8_blocks(N) : (N + bn - 1) / bn; };
-    pl->ctas = pl->cl = 1;
-    if (M > FP8_BM && (rows + 1) / 2 * cols(256) >= num_sms / 2) {
-        pl->bn = 256;
+    const long long cols = fp8_blocks(N), wide = gated ? cols : (N + 255) / 256;     // columns in 128s, in pairs' tiles
+    pl->bn = gated ? 256 : 128;
+    pl->ctas = pl->split = 1;
+    if (M > FP8_BM && (rows + 1) / 2 * wide >= num_sms / 2) {
+        pl->bn = 256;                           // pairs, at least one wave of them
         pl->ctas = 2;
         rows = (rows + 1) / 2;
-    } else if (gated) {
-        pl->bn = rows * cols(64) * 4 >= num_sms ? 64 : 32;
-        pl->cl = FP8_BLOCK / (pl->bn / 2);
-    } else {
-        pl->bn = rows * cols(128) >= num_sms ? 128 : rows * cols(64) >= num_sms ? 64 : 32;
     }
-    const long long tiles = rows * cols(pl->bn);
-    if (tiles > (1 << 30)) return false;
+    const long long tiles = rows * (pl->ctas == 2 ? wide : cols);
+    if (tiles > (1 << 27)) return false;
+    if (pl->ctas == 1) {
+        const int kb = fp8_blocks(K);
+        for (int n = 2; n <= FP8_SPLIT_MAX && n <= kb && tiles <= clusters[n]; ++n) pl->split = n;
+    }
+    const int split = pl->split > 1 || (gated && pl->ctas == 1);      // the split form (also with one CTA)
     pl->m_tiles = (int)rows;
     pl->tiles = (int)tiles;
     pl->a_rows = M < FP8_BM ? (M + 7) / 8 * 8 : FP8_BM;
-    pl->tmem_cols = fp8_bufs(pl->bn) * pl->bn;
-    pl->smem = fp8_smem_bytes(pl->bn);
     // Where the two MMA warps take every other K block, an even number of stages keeps a stage with one
     // of them: a warp that met only every other use of a barrier could take a phase for the one before
     // or after it (a wait tells them apart by parity alone).
     const int by = fp8_split(pl->bn) == 2 ? 1 : 2;
     int ns = FP8_STAGES_MAX;
-    while (ns > 2 && fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) ns -= by;
-    if (fp8_smem(pl->bn, pl->ctas, pl->cl, gated, pl->a_rows, ns).total > pl->smem) return false;
+    while (ns > 2 && fp8_smem(pl->bn, pl->ctas, gated, split, pl->a_rows, ns).total > FP8_SMEM_SM) ns -= by;
+    if (fp8_smem(pl->bn, pl->ctas, gated, split, pl->a_rows, ns).total > FP8_SMEM_SM) return false;
     pl->n_stages = ns;
-    const int group = pl->ctas == 2 ? 2 : pl->cl;
-    const long long most = (long long)num_sms * fp8_ctas_per_sm(pl->bn) / group;     // clusters that fit at once
-    pl->grid = (int)(tiles < most ? tiles : most) * group;
+    if (split) {
+        pl->grid = (int)tiles * pl->split;      // a cluster per tile
+    } else {
+        const long long most = num_sms / pl->ctas;
+        pl->grid = (int)(tiles < most ? tiles : most) * pl->ctas;
+    }
     return true;
 }
 

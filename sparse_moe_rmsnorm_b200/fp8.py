@@ -73,8 +73,7 @@ def moe_fp8_gated_matmul(ctx, M, F, K, a, lda, a_scale, w13, w13_scale, b13, alp
                 "moe_fp8_gated_matmul")
 
 
-FP8_PLAN_FIELDS = ("bn", "ctas", "cluster", "a_rows", "n_stages", "m_tiles", "tiles", "grid", "smem", "smem_needed",
-                   "tmem_cols", "ctas_per_sm")
+FP8_PLAN_FIELDS = ("few", "bn", "ctas", "split", "a_rows", "n_stages", "m_tiles", "tiles", "grid", "smem_needed")
 
 
 def moe_fp8_debug_plan(gated: bool, M: int, N: int, K: int, num_sms: int) -> Dict[str, int]:
