@@ -293,23 +293,22 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
     constexpr int TMA_WARP = WGS * 4, MMA_WARP = TMA_WARP + 1, SCALE_WARP = TMA_WARP + 3;
     constexpr uint32_t COLS = BUFS * BN;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);             // the (even CTA's) producer
-            mbar_init(&empty[i], SPLIT);        // MMA commits
+    if (warp == TMA_WARP) {                     // (a lane a barrier: one thread after another took 0.2 us)
+        if (lane < NS) {
+            mbar_init(&full[lane], 1);          // the (even CTA's) producer
+            mbar_init(&empty[lane], SPLIT);     // MMA commits
         }
-        for (int i = 0; i < SPLIT * BUFS; ++i) {
-            mbar_init(&d_full[i], 1);           // MMA commit
-            mbar_init(&d_empty[i], WGS / SPLIT * 4 * CTAS);   // every epilogue warp that reads it (of both CTAs)
+        if (lane < SPLIT * BUFS) {
+            mbar_init(&d_full[lane], 1);        // MMA commit
+            mbar_init(&d_empty[lane], WGS / SPLIT * 4 * CTAS);    // every epilogue warp that reads it (of both CTAs)
         }
-        mbar_init(&drain_bar[0], 1);
-        mbar_init(&drain_bar[1], 1);
-        for (int i = 0; i < 8; ++i) mbar_init(&ex_bar[i], WGS);
-        for (int i = 0; i < FP8_CHUNKS; ++i) {
-            mbar_init(&sc_full[i], 32);         // every lane of the scale warp
-            mbar_init(&sc_empty[i], WGS * 4);   // every epilogue warp
+        if (lane < 2) mbar_init(&drain_bar[lane], 1);
+        if (lane < 8) mbar_init(&ex_bar[lane], WGS);
+        if (lane < FP8_CHUNKS) {
+            mbar_init(&sc_full[lane], 32);      // every lane of the scale warp
+            mbar_init(&sc_empty[lane], WGS * 4);    // every epilogue warp
         }
-        *abort_s = 0;
+        if (lane == 0) *abort_s = 0;
         fence_barrier_init();
     }
     if (warp == MMA_WARP) tmem_alloc_g<CTAS>(tmem_base_s, COLS);
@@ -317,7 +316,6 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
     __syncthreads();
     if constexpr (CTAS > 1) cluster_sync();     // the peer's barriers are initialised
     tc_fence_after();
-    pdl_wait();
     pdl_trigger();
     const uint32_t tmem = *tmem_base_s;
     const WaitCtl wc{abort_s, p.err, FP8_ERR_WAIT, p.wait_limit_ns};
@@ -337,6 +335,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
             const uint32_t a_stage = plan.a_stage, b_stage = plan.b_stage;
             const uint32_t bytes = CTAS * (a_stage + b_stage);
             const int tiles = p.tiles, m_tiles = p.m_tiles;
+            pdl_wait();                                 // (each role where it first touches a predecessor's memory)
             int slot = 0;
             uint32_t ph = 0, fills = 0;                 // fills: at most NS are of interest
             bool ok = true;
@@ -417,6 +416,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
             constexpr int RPI = 32 / FP8_CHUNK;                 // rows per instruction
             const uint32_t full0 = smem_addr(sc_full), empty0 = smem_addr(sc_empty);
             const uint32_t dst0 = scales0 + (uint32_t)lane * 4;
+            pdl_wait();
             int cb = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
                 else mbar_arrive_at(bar);
             }
         };
+        pdl_wait();
         for (int t = first; t < p.tiles && ok; t += step) {
             // first row and column of the warp's part of the tile
             const int nt = t / p.m_tiles;
@@ -605,12 +606,17 @@ static cudaError_t launch_t(const Fp8GemmParams &p, const Fp8Plan &pl, cudaStrea
     attr[1].val.clusterDim.x = SK ? pl.split : CTAS;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CTAS == 2 || SK ? 2 : 1;
+    cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN, CTAS, GATED, SK>, p);
 }
 
 template <int BN, int CTAS, bool GATED, bool SK>
 static cudaError_t setup_t() {
+    // the registers that the kernel's warpgroups share out have to be there at launch
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, fp8_gemm_kernel<BN, CTAS, GATED, SK>);
+    if (e == cudaSuccess && attr.numRegs != 168) e = cudaErrorInvalidKernelImage;
+    if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(fp8_gemm_kernel<BN, CTAS, GATED, SK>, cudaFuncAttributeMaxDynamicSharedMemorySize, FP8_SMEM_SM);
 }
 
