@@ -77,11 +77,11 @@ struct Pack {
 
 // The staged sums (+ bias) (+ residual), rounded once, to rows m0.. and columns n0.. of c; lane i brings the
 // bias of column n0 + i.  V == 4: 32 whole rows, four elements per lane; V == 1: what there is, a column per
-// lane.  Four steps at a time, their residuals first; every element of the residual is read by the thread that
+// lane.  Several steps at a time, their residuals first; every element of the residual is read by the thread that
 // writes c's, so the two may be the same.
 template <typename T, int CC, int V, bool RES>
 __device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *tile, float bias, int m0, int n0, int lane) {
-    constexpr int LPR = CC / V, RPI = 32 / LPR;              // lanes per row, rows per step
+    constexpr int LPR = CC / V, RPI = 32 / LPR, B = V == 1 && RES ? 8 : 4;     // lanes per row, rows per step, steps at a time
     typedef decltype(Pack<T, V>::raw) Raw;
     const int pc = lane % LPR, r0 = lane / LPR, col = n0 + V * pc;
     float b[V];
@@ -93,15 +93,15 @@ __device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *ti
     const long long cs = RPI * p.ldc, rs = RPI * p.ldr;
     const float *f = tile + r0 * (CC + 4) + V * pc;
 #pragma unroll 1
-    for (int r = r0; r < rows; r += 4 * RPI, f += 4 * RPI * (CC + 4)) {
-        Pack<T, V> old[4];
+    for (int r = r0; r < rows; r += B * RPI, f += B * RPI * (CC + 4)) {
+        Pack<T, V> old[B];
         if constexpr (RES) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i, res += rs)
+            for (int i = 0; i < B; ++i, res += rs)
                 if (V == 4 || r + i * RPI < rows) old[i].raw = *reinterpret_cast<const Raw *>(res);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i, c += cs) {
+        for (int i = 0; i < B; ++i, c += cs) {
             if (V == 4 || r + i * RPI < rows) {
                 float o[V];
                 if constexpr (V == 4) {
@@ -123,21 +123,18 @@ __device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *ti
     }
 }
 
-template <typename T, int CC>
+template <typename T, int CC, bool RES>
 __device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *tile, float bias, int m0, int n0, int lane) {
-    if (p.vec && m0 + 32 <= p.M && n0 + CC <= p.N) {
-        if (p.residual) put_tile<T, CC, 4, true>(p, tile, bias, m0, n0, lane);
-        else put_tile<T, CC, 4, false>(p, tile, bias, m0, n0, lane);
-    } else {
-        if (p.residual) put_tile<T, CC, 1, true>(p, tile, bias, m0, n0, lane);
-        else put_tile<T, CC, 1, false>(p, tile, bias, m0, n0, lane);
-    }
+    if (p.vec && m0 + 32 <= p.M && n0 + CC <= p.N) put_tile<T, CC, 4, RES>(p, tile, bias, m0, n0, lane);
+    else put_tile<T, CC, 1, RES>(p, tile, bias, m0, n0, lane);
 }
 
 // A warp's sums, CC columns at a time: each thread's row into the staging tile, rows out of it.  The loop over
-// the parts stays a loop (its body is every part's): code that runs once a tile does not stay in the
-// instruction caches, and unrolled for each type it took longer to fetch than to run.
-template <int CW, int CC>
+// the parts stays a loop (its body is every part's), and the residual has kernels of its own: code that runs once
+// a tile does not stay in the instruction caches, and the largest products lost 4% to a second copy of put_tile.
+// (Measured against this staging: 128 bytes of a row at a time in c's type, unrolled, 6% longer on narrow tiles;
+// 16-byte pieces of 32 rows straight from the registers 30% longer.)
+template <int CW, int CC, bool RES>
 __device__ __forceinline__ void store_columns(const Fp8GemmParams &p, const float (&acc)[CW], const float (&bias)[(CW + 31) / 32],
                                               float *tile, int m0, int n0, int lane) {
 #pragma unroll 1
@@ -154,34 +151,36 @@ __device__ __forceinline__ void store_columns(const Fp8GemmParams &p, const floa
                 b = bias[s * CC / 32];
             }
         __syncwarp();
-        if (p.type == FP8_BF16) put_tile<__nv_bfloat16, CC>(p, tile, b, m0, n0 + part * CC, lane);
-        else if (p.type == FP8_FP16) put_tile<__half, CC>(p, tile, b, m0, n0 + part * CC, lane);
-        else put_tile<float, CC>(p, tile, b, m0, n0 + part * CC, lane);
+        if (p.type == FP8_BF16) put_tile<__nv_bfloat16, CC, RES>(p, tile, b, m0, n0 + part * CC, lane);
+        else if (p.type == FP8_FP16) put_tile<__half, CC, RES>(p, tile, b, m0, n0 + part * CC, lane);
+        else put_tile<float, CC, RES>(p, tile, b, m0, n0 + part * CC, lane);
         __syncwarp();
     }
 }
 
+// (Volatile keeps it behind the cluster barrier; no memory clobber, so that a round's loads stay together.)
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 
-// The sum over the cluster's CTAs, in their order, of four neighbouring sums at byte `at` of their tiles.
-__device__ __forceinline__ float4 parts_sum(uint32_t tile, uint32_t at, int split) {
+// Four neighbouring sums at byte `at` of every CTA's tile, and their sum in the CTAs' order.
+struct Parts {
     float4 v[FP8_SPLIT_MAX];
+    __device__ __forceinline__ void load(uint32_t tile, uint32_t at, int split) {
 #pragma unroll
-    for (int c = 0; c < FP8_SPLIT_MAX; ++c)
-        if (c < split) v[c] = ld_cluster_f32x4(map_to_rank(tile + at, (uint32_t)c));
-    float4 t = v[0];
+        for (int c = 0; c < FP8_SPLIT_MAX; ++c)
+            if (c < split) v[c] = ld_cluster_f32x4(map_to_rank(tile + at, (uint32_t)c));
+    }
+    __device__ __forceinline__ float4 sum(int split) const {
+        float4 t = v[0];
 #pragma unroll
-    for (int c = 1; c < FP8_SPLIT_MAX; ++c)
-        if (c < split) t.x += v[c].x, t.y += v[c].y, t.z += v[c].z, t.w += v[c].w;
-    return t;
-}
+        for (int c = 1; c < FP8_SPLIT_MAX; ++c)
+            if (c < split) t.x += v[c].x, t.y += v[c].y, t.z += v[c].z, t.w += v[c].w;
+        return t;
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void put_four(const Fp8GemmParams &p, long long row, int n, float (&o)[4]) {
@@ -216,22 +215,35 @@ __device__ __forceinline__ void join_parts(const Fp8GemmParams &p, uint32_t tile
     for (int h = 0; h < (GATED ? 2 : 1); ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[h][j] = p.bias && n + j < p.N ? bf16_bits_to_f32(p.bias[h * p.N + n + j]) : 0.0f;
+    const int end = min(rows, (rank + 1) * each);
+    // plain: two rows at a time, gated: a row's gate and linear sums, so that 16 remote loads are in flight
+    constexpr int STEP = FP8_WGS * 4;
 #pragma unroll 1
-    for (int r = rank * each + warp; r < min(rows, (rank + 1) * each); r += FP8_WGS * 4) {
-        const uint32_t row = (uint32_t)(r * (BN + 4)) * 4;
-        const long long m = m0 + r;
+    for (int r = rank * each + warp; r < end; r += GATED ? STEP : 2 * STEP) {
+        Parts x, y;
         if constexpr (!GATED) {
-            const float4 v = parts_sum(tile, row + 16 * lane, p.split);
+            const uint32_t at = (uint32_t)(r * (BN + 4) + 4 * lane) * 4;
+            x.load(tile, at, p.split);
+            if (r + STEP < end) y.load(tile, at + STEP * (BN + 4) * 4, p.split);
             if (n >= p.N) continue;
-            float o[4] = {v.x + b[0][0], v.y + b[0][1], v.z + b[0][2], v.w + b[0][3]};
-            if (p.type == FP8_BF16) put_four<__nv_bfloat16>(p, m, n, o);
-            else if (p.type == FP8_FP16) put_four<__half>(p, m, n, o);
-            else put_four<float>(p, m, n, o);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (r + i * STEP >= end) break;
+                const long long m = m0 + r + i * STEP;
+                const float4 v = i ? y.sum(p.split) : x.sum(p.split);
+                float o[4] = {v.x + b[0][0], v.y + b[0][1], v.z + b[0][2], v.w + b[0][3]};
+                if (p.type == FP8_BF16) put_four<__nv_bfloat16>(p, m, n, o);
+                else if (p.type == FP8_FP16) put_four<__half>(p, m, n, o);
+                else put_four<float>(p, m, n, o);
+            }
         } else {
             // a warpgroup's columns are 64 gate and 64 linear ones
-            const uint32_t at = row + (uint32_t)(lane / 16 * 128 + lane % 16 * 4) * 4;
-            const float4 gv = parts_sum(tile, at, p.split), uv = parts_sum(tile, at + 256, p.split);
+            const uint32_t at = (uint32_t)(r * (BN + 4) + lane / 16 * 128 + lane % 16 * 4) * 4;
+            x.load(tile, at, p.split);
+            y.load(tile, at + 256, p.split);
+            const float4 gv = x.sum(p.split), uv = y.sum(p.split);
             const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, us[4] = {uv.x, uv.y, uv.z, uv.w};
+            const long long m = m0 + r;
             float h[4], amax = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -258,11 +270,12 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity, unsig
 
 }  // namespace
 
-template <int BN, int CTAS, bool GATED, bool SK>
+// RES: with a residual (a kernel of its own, as its code made the others' slower: see store_columns).
+template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr int WGS = FP8_WGS;                // epilogue warpgroups
     constexpr int CW = BN / WGS;                // accumulator columns per epilogue thread
-    constexpr int LD = 16;                      // columns of a TMEM load (registers: 2 LD beside the CW sums)
+    constexpr int LD = CW > 64 && !GATED ? 32 : 16;     // columns of a TMEM load (registers: 2 LD beside the CW sums)
     constexpr int CC = FP8_TILE_COLS;           // columns of a staging tile
     constexpr int HW = CW / 2;                  // gated: h columns per thread
     constexpr int BUFS = fp8_bufs(BN);
@@ -483,6 +496,15 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
                 const int i = 32 * j + lane, col = n0 + (GATED ? i % HW : i);
                 bias[j] = !SK && p.bias && col < p.N ? bf16_bits_to_f32(p.bias[(GATED && i >= HW ? p.N : 0) + col]) : 0.0f;
             }
+            if constexpr (RES) {
+                // the residual's part of this lane's row starts on its way to L2: read after the sums, from memory, it
+                // took 6 us a tile
+                if (active && m0 + lane < p.M) {
+                    const int eb = p.type == FP8_FP32 ? 4 : 2, bytes = min(CW, p.N - n0) * eb;
+                    const char *row = static_cast<const char *>(p.residual) + ((m0 + lane) * p.ldr + n0) * eb;
+                    for (int i = 0; i < bytes; i += 128) prefetch_l2(row + i);
+                }
+            }
             float acc[CW];
 #pragma unroll
             for (int i = 0; i < CW; ++i) acc[i] = 0.0f;
@@ -575,7 +597,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
                     if (n0 % FP8_BLOCK == 0) p.h_scale[(long long)(m0 + lane) * p.NB + n0 / FP8_BLOCK] = s;
                 }
             } else if (!SK && active) {
-                store_columns<CW, CC>(p, acc, bias, reinterpret_cast<float *>(smem + plan.stage_off + warp * fp8_tile_bytes(0)), m0, n0, lane);
+                store_columns<CW, CC, RES>(p, acc, bias, reinterpret_cast<float *>(smem + plan.stage_off + warp * fp8_tile_bytes(0)), m0, n0, lane);
             }
         }
         if constexpr (SK) {
@@ -592,7 +614,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
     if (warp == MMA_WARP) tmem_dealloc_g<CTAS>(tmem, COLS);
 }
 
-template <int BN, int CTAS, bool GATED, bool SK>
+template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 static cudaError_t launch_t(const Fp8GemmParams &p, const Fp8Plan &pl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pl.grid);
@@ -607,27 +629,29 @@ static cudaError_t launch_t(const Fp8GemmParams &p, const Fp8Plan &pl, cudaStrea
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = attr[1].val.clusterDim.x > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN, CTAS, GATED, SK>, p);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN, CTAS, GATED, SK, RES>, p);
 }
 
-template <int BN, int CTAS, bool GATED, bool SK>
+template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 static cudaError_t setup_t() {
     // the registers that the kernel's warpgroups share out have to be there at launch
     cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, fp8_gemm_kernel<BN, CTAS, GATED, SK>);
+    cudaError_t e = cudaFuncGetAttributes(&attr, fp8_gemm_kernel<BN, CTAS, GATED, SK, RES>);
     if (e == cudaSuccess && attr.numRegs != 168) e = cudaErrorInvalidKernelImage;
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fp8_gemm_kernel<BN, CTAS, GATED, SK>, cudaFuncAttributeMaxDynamicSharedMemorySize, FP8_SMEM_SM);
+    return cudaFuncSetAttribute(fp8_gemm_kernel<BN, CTAS, GATED, SK, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, FP8_SMEM_SM);
 }
 
 // Once per device, before the first launch: the kernels' shared memory, and how many clusters of 1 to
 // FP8_SPLIT_MAX CTAs the device holds at once (an SM to a CTA; a cluster lies in one GPC).
 cudaError_t fp8_gemm_setup(int *clusters) {
-    cudaError_t e = setup_t<128, 1, false, false>();
-    if (e == cudaSuccess) e = setup_t<128, 1, false, true>();
-    if (e == cudaSuccess) e = setup_t<256, 1, true, true>();
-    if (e == cudaSuccess) e = setup_t<256, 2, false, false>();
-    if (e == cudaSuccess) e = setup_t<256, 2, true, false>();
+    cudaError_t e = setup_t<128, 1, false, false, false>();
+    if (e == cudaSuccess) e = setup_t<128, 1, false, false, true>();
+    if (e == cudaSuccess) e = setup_t<128, 1, false, true, false>();
+    if (e == cudaSuccess) e = setup_t<256, 1, true, true, false>();
+    if (e == cudaSuccess) e = setup_t<256, 2, false, false, false>();
+    if (e == cudaSuccess) e = setup_t<256, 2, false, false, true>();
+    if (e == cudaSuccess) e = setup_t<256, 2, true, false, false>();
     for (int n = 1; n <= FP8_SPLIT_MAX && e == cudaSuccess; ++n) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n);
@@ -639,15 +663,16 @@ cudaError_t fp8_gemm_setup(int *clusters) {
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&clusters[n], fp8_gemm_kernel<128, 1, false, true>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&clusters[n], fp8_gemm_kernel<128, 1, false, true, false>, &cfg);
     }
     return e;
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s) {
-    if (gated) return pl.ctas == 2 ? launch_t<256, 2, true, false>(p, pl, s) : launch_t<256, 1, true, true>(p, pl, s);
-    if (pl.ctas == 2) return launch_t<256, 2, false, false>(p, pl, s);
-    return pl.split > 1 ? launch_t<128, 1, false, true>(p, pl, s) : launch_t<128, 1, false, false>(p, pl, s);
+    if (gated) return pl.ctas == 2 ? launch_t<256, 2, true, false, false>(p, pl, s) : launch_t<256, 1, true, true, false>(p, pl, s);
+    if (pl.split > 1) return launch_t<128, 1, false, true, false>(p, pl, s);       // (the residual is join_parts')
+    if (pl.ctas == 2) return p.residual ? launch_t<256, 2, false, false, true>(p, pl, s) : launch_t<256, 2, false, false, false>(p, pl, s);
+    return p.residual ? launch_t<128, 1, false, false, true>(p, pl, s) : launch_t<128, 1, false, false, false>(p, pl, s);
 }
 
 }  // namespace moe

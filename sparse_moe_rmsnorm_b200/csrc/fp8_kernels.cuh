@@ -40,7 +40,7 @@ struct Fp8GemmParams {
     void *c;                        // type [M, N], rows ldc elements apart
     long long ldr, ldc;
     int type;                       // FP8_BF16, FP8_FP16 or FP8_FP32
-    int vec;                        // four elements of a row of c (and of the residual) move as one
+    int vec;                        // rows of c (and of the residual) start on 16 bytes
     float minus_alpha_log2e, limit, shift;      // gated activation
     uint8_t *h;                     // gated: E4M3 [M, F]
     float *h_scale;                 // gated: [M, NB]
@@ -98,9 +98,9 @@ constexpr int FP8_CHUNK = 4, FP8_CHUNKS = 4;
 constexpr int FP8_CHUNK_BYTES = (FP8_BM + 2) * FP8_CHUNK * 4;
 constexpr int FP8_SCALE_BYTES = FP8_CHUNKS * FP8_CHUNK_BYTES;
 // An epilogue warp's staging tile: 32 rows of 32 sums, rows 16 bytes further apart than they are long
-// (gated: the biases of its 128 columns).
+// (gated: the biases of its 128 columns; a split tile: none).
 constexpr int FP8_TILE_COLS = 32;
-__host__ __device__ constexpr int fp8_tile_bytes(int gated) { return gated ? 128 * 4 : 32 * (FP8_TILE_COLS + 4) * 4; }     // (a split tile: none)
+__host__ __device__ constexpr int fp8_tile_bytes(int gated) { return gated ? 128 * 4 : 32 * (FP8_TILE_COLS + 4) * 4; }
 
 // Offsets from a 1024-aligned base: the A ring, the B ring, each epilogue warp's staging tile, the
 // scales, the barriers, the row maxima that warps exchange, the TMEM base and abort flag.
@@ -137,19 +137,26 @@ inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, const int *clu
     if (M > FP8_SIZE_MAX || N > FP8_SIZE_MAX || K > FP8_SIZE_MAX) return false;
     long long rows = (M + FP8_BM - 1) / FP8_BM;
     const long long cols = fp8_blocks(N), wide = gated ? cols : (N + 255) / 256;     // columns in 128s, in pairs' tiles
+    // The form that should take least: us per K block (of hand-overs, mostly) and per tile, as measured
+    const int kb = fp8_blocks(K);
+    auto waves = [](long long tiles, int at_once) { return (double)((tiles + at_once - 1) / at_once); };
+    const long long pair_tiles = (rows + 1) / 2 * wide, one_tiles = rows * cols;
+    int n = 1;                                  // CTAs to split K over
+    while (n < FP8_SPLIT_MAX && n < kb && one_tiles <= clusters[n + 1]) ++n;
+    const double per_kb = gated ? 0.6 : 0.37, pair = waves(pair_tiles, num_sms / 2) * (0.55 * kb + 3.0);
+    const double one = n > 1 || gated ? waves(one_tiles, clusters[n]) * (per_kb * ((kb + n - 1) / n) + 4.0)
+                                      : waves(one_tiles, num_sms) * (per_kb * kb + 2.0);
     pl->bn = gated ? 256 : 128;
-    pl->ctas = pl->split = 1;
-    if (M > FP8_BM && (rows + 1) / 2 * wide >= num_sms / 2) {
-        pl->bn = 256;                           // pairs, at least one wave of them
+    pl->ctas = 1;
+    pl->split = n;
+    if (M > FP8_BM && pair < one) {
+        pl->bn = 256;
         pl->ctas = 2;
+        pl->split = 1;
         rows = (rows + 1) / 2;
     }
-    const long long tiles = rows * (pl->ctas == 2 ? wide : cols);
+    const long long tiles = pl->ctas == 2 ? pair_tiles : one_tiles;
     if (tiles > (1 << 27)) return false;
-    if (pl->ctas == 1) {
-        const int kb = fp8_blocks(K);
-        for (int n = 2; n <= FP8_SPLIT_MAX && n <= kb && tiles <= clusters[n]; ++n) pl->split = n;
-    }
     const int split = pl->split > 1 || (gated && pl->ctas == 1);      // the split form (also with one CTA)
     pl->m_tiles = (int)rows;
     pl->tiles = (int)tiles;
