@@ -281,9 +281,11 @@ typedef struct moe_fp8_ctx moe_fp8_ctx_t;
 MOE_API int moe_fp8_init(moe_fp8_ctx_t **out);
 MOE_API int moe_fp8_destroy(moe_fp8_ctx_t *ctx);
 
-/* As moe_sync_status and moe_set_wait_limit_ns. */
+/* As moe_sync_status, moe_set_wait_limit_ns and moe_selftest_wait_timeout.  (A context's
+ * calls may be captured from the first on; the status is asked for outside a capture.) */
 MOE_API int moe_fp8_sync_status(moe_fp8_ctx_t *ctx, void *stream);
 MOE_API int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *ctx, unsigned long long ns);
+MOE_API int moe_fp8_selftest_wait_timeout(moe_fp8_ctx_t *ctx, void *stream);
 
 /* n = x + residual (residual may be NULL: n = x), in fp32;
  * sum_out = n rounded to `type` (may be NULL, and is without a residual; may be x
@@ -309,7 +311,7 @@ MOE_API int moe_fp8_matmul(moe_fp8_ctx_t *ctx, int M, int N, int K, const uint8_
  *   g = min(W13_gate a + b_gate, limit),  u = clamp(W13_linear a + b_linear, -limit, limit),
  *   h = g * sigmoid(alpha g) * (u + shift), then E4M3 with a scale per 128 columns.
  * (alpha, limit, shift) = (1.702, 7, 1) is the experts' activation, (1, INFINITY, 0) is
- * silu(gate) * linear.  a, a_scale as above; w13 u8 [2, F, K] (gate rows, then linear rows),
+ * silu(gate) * linear; alpha and shift are finite, limit > 0.  a, a_scale as above; w13 u8 [2, F, K] (gate rows, then linear rows),
  * w13_scale fp32 [2, ceil(F/128), ceil(K/128)] (each half has its own blocks), b13 bf16
  * [2, F] or NULL; h u8 [M, F], h_scale fp32 [M, ceil(F/128)].  F a multiple of 16. */
 MOE_API int moe_fp8_gated_matmul(moe_fp8_ctx_t *ctx, int M, int F, int K, const uint8_t *a, int64_t lda,

@@ -25,8 +25,8 @@ __all__ = [
     "moe_selftest_wait_timeout", "moe_debug_decode", "moe_debug_plan", "moe_strerror", "moe_version", "WS",
     "moe_forward_noalloc", "MOE_NOALLOC_MAX_TOKENS",
     "MOE_BF16", "MOE_FP16", "MOE_FP32", "Fp8Ops", "DenseFFN", "DenseWeights", "quantize_fp8_rows", "quantize_fp8_weight",
-    "moe_fp8_init", "moe_fp8_destroy", "moe_fp8_sync_status", "moe_fp8_set_wait_limit_ns", "moe_add_rmsnorm_fp8",
-    "moe_fp8_matmul", "moe_fp8_gated_matmul", "moe_fp8_debug_plan",
+    "moe_fp8_init", "moe_fp8_destroy", "moe_fp8_sync_status", "moe_fp8_set_wait_limit_ns",
+    "moe_fp8_selftest_wait_timeout", "moe_add_rmsnorm_fp8", "moe_fp8_matmul", "moe_fp8_gated_matmul", "moe_fp8_debug_plan",
 ]
 
 MOE_NOALLOC_MAX_TOKENS = 64
@@ -81,6 +81,7 @@ _SIGS = {
     "moe_fp8_destroy": (ctypes.c_int, [ctypes.c_void_p]),
     "moe_fp8_sync_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "moe_fp8_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_ulonglong]),
+    "moe_fp8_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "moe_add_rmsnorm_fp8": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 3
                             + [ctypes.c_void_p, ctypes.c_int64] * 2 + [ctypes.c_void_p, ctypes.c_float]
                             + [ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 3),
@@ -381,6 +382,6 @@ class MoE:
 
 from .fp8 import (  # noqa: E402  (it calls this module's helpers)
     MOE_BF16, MOE_FP16, MOE_FP32, DenseFFN, DenseWeights, Fp8Ops, moe_add_rmsnorm_fp8, moe_fp8_debug_plan,
-    moe_fp8_destroy, moe_fp8_gated_matmul, moe_fp8_init, moe_fp8_matmul, moe_fp8_set_wait_limit_ns,
-    moe_fp8_sync_status, quantize_fp8_rows, quantize_fp8_weight,
+    moe_fp8_destroy, moe_fp8_gated_matmul, moe_fp8_init, moe_fp8_matmul, moe_fp8_selftest_wait_timeout,
+    moe_fp8_set_wait_limit_ns, moe_fp8_sync_status, quantize_fp8_rows, quantize_fp8_weight,
 )

@@ -2,6 +2,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <new>
@@ -13,6 +14,9 @@
 namespace moe {
 cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, int num_sms, cudaStream_t s);
 cudaError_t fp8_gemm_setup(int *clusters);
+cudaError_t fp8_few_setup();
+cudaError_t fp8_norm_setup();
+cudaError_t launch_selftest_wait(unsigned int *err, unsigned long long limit_ns, cudaStream_t s);
 cudaError_t launch_fp8_few(const Fp8FewParams &p, int gated, cudaStream_t s);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s);
 }  // namespace moe
@@ -142,7 +146,8 @@ int moe_fp8_init(moe_fp8_ctx_t **out) {
     c->num_sms = sms;
     c->wait_limit_ns = 2000000000ull;
     memset(c->clusters, 0, sizeof c->clusters);
-    if (fp8_gemm_setup(c->clusters) != cudaSuccess) {
+    // (every kernel is loaded here, so that a first call may be captured)
+    if (fp8_gemm_setup(c->clusters) != cudaSuccess || fp8_few_setup() != cudaSuccess || fp8_norm_setup() != cudaSuccess) {
         delete c;
         return MOE_ERR_CUDA;
     }
@@ -188,6 +193,13 @@ int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *c, unsigned long long ns) {
     if (!c || ns == 0) return MOE_ERR_ARG;
     c->wait_limit_ns = ns;
     return MOE_OK;
+}
+
+int moe_fp8_selftest_wait_timeout(moe_fp8_ctx_t *c, void *stream) {
+    if (!c) return MOE_ERR_ARG;
+    DeviceGuard g(c->device);
+    if (!g.ok) return MOE_ERR_CUDA;
+    return status(launch_selftest_wait(c->err, c->wait_limit_ns, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *c, int T, int d, int type, const void *x, int64_t ldx, const void *residual,
@@ -259,7 +271,7 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
                          const uint8_t *w13, const float *w13_scale, const uint16_t *b13, float alpha, float limit,
                          float shift, uint8_t *h, float *h_scale, void *stream) {
     int rc = check_product(c, M, F, K, a, lda, a_scale, w13, w13_scale, b13);
-    if (rc || F % 16 || !(limit > 0.0f) || alpha != alpha || shift != shift) return MOE_ERR_ARG;
+    if (rc || F % 16 || !(limit > 0.0f) || !std::isfinite(alpha) || !std::isfinite(shift)) return MOE_ERR_ARG;
     if (M == 0) return MOE_OK;
     if (!aligned(h, 16) || !aligned(h_scale, 4)) return MOE_ERR_ARG;
     DeviceGuard g(c->device);

@@ -269,6 +269,16 @@ static cudaError_t launch_few_t(const Fp8FewParams &p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, fp8_few_kernel<NT, GATED>, p);
 }
 
+// Loads the kernels (once per device, before the first launch, which may be captured).
+cudaError_t fp8_few_setup() {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, fp8_few_kernel<1, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, fp8_few_kernel<2, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, fp8_few_kernel<1, true>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, fp8_few_kernel<2, true>);
+    return e;
+}
+
 cudaError_t launch_fp8_few(const Fp8FewParams &p, int gated, cudaStream_t s) {
     if (gated) return p.M <= 8 ? launch_few_t<1, true>(p, s) : launch_few_t<2, true>(p, s);
     return p.M <= 8 ? launch_few_t<1, false>(p, s) : launch_few_t<2, false>(p, s);

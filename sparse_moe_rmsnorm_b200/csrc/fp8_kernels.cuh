@@ -139,7 +139,7 @@ inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, const int *clu
     const long long cols = fp8_blocks(N), wide = gated ? cols : (N + 255) / 256;     // columns in 128s, in pairs' tiles
     // The form that should take least: us per K block (of hand-overs, mostly) and per tile, as measured
     const int kb = fp8_blocks(K);
-    auto waves = [](long long tiles, int at_once) { return (double)((tiles + at_once - 1) / at_once); };
+    auto waves = [](long long tiles, int at_once) { return at_once > 0 ? (double)((tiles + at_once - 1) / at_once) : 1e30; };
     const long long pair_tiles = (rows + 1) / 2 * wide, one_tiles = rows * cols;
     int n = 1;                                  // CTAs to split K over
     while (n < FP8_SPLIT_MAX && n < kb && one_tiles <= clusters[n + 1]) ++n;

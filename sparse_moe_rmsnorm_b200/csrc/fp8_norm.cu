@@ -7,9 +7,10 @@
 // "gpt-oss-20B" hub page, section 3.2) and stands beside it: here the rows leave in the form the
 // dense 8-bit products read.  Bound by HBM: x, r, the sum and q move once (8192 rows of 2880, bf16:
 // 166 MB in 28.0 us, 0.90 of the measured copy rate), and next by instruction issue: the arithmetic is on
-// pairs (f32x2), which took it from 39 us.  One CTA holds a row in registers, 8 elements (or several times 8) per thread, so the row is read once
-// and the second pass (the scaling) needs no memory; a block's 128 elements sit in 16 neighbouring
-// lanes, so its maximum is four shuffles.
+// pairs (f32x2), which took it from 39 us.  One CTA holds a row in registers, 8 or 16 elements per
+// thread, so the row is read once and the second pass (the scaling) needs no memory; a block's 128
+// elements sit in 16 neighbouring lanes, so its maximum is four shuffles.  A row's sum adds the
+// elements of a thread in two halves, then a tree over lanes and warps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -201,6 +202,24 @@ static cudaError_t launch_norm_t(const Fp8NormParams &p, int num_sms, cudaStream
     // an SM.  Measured (bf16, d = 2880, residual; one, two, three pieces): T = 600 4.6, 5.4, 5.4 us; T = 1024 6.3
     // all three; T = 8192 31.1, 28.0, 27.7 us; T = 2048, d = 6144 20.4, 16.4, 16.7 us.
     return pieces > 1024 || p.T >= 8 * num_sms ? launch_norm_ch<T, 2>(p, s) : launch_norm_ch<T, 1>(p, s);
+}
+
+template <typename T>
+static cudaError_t load_t() {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, add_rmsnorm_fp8_kernel<T, 1, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, add_rmsnorm_fp8_kernel<T, 1, true>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, add_rmsnorm_fp8_kernel<T, 2, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, add_rmsnorm_fp8_kernel<T, 2, true>);
+    return e;
+}
+
+// Loads the kernels (once per device, before the first launch, which may be captured).
+cudaError_t fp8_norm_setup() {
+    cudaError_t e = load_t<__nv_bfloat16>();
+    if (e == cudaSuccess) e = load_t<__half>();
+    if (e == cudaSuccess) e = load_t<float>();
+    return e;
 }
 
 cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, int num_sms, cudaStream_t s) {

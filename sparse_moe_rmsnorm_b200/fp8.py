@@ -20,8 +20,8 @@ import sparse_moe_rmsnorm_b200 as _moe
 
 __all__ = [
     "MOE_BF16", "MOE_FP16", "MOE_FP32", "Fp8Ops", "DenseFFN", "DenseWeights", "quantize_fp8_rows", "quantize_fp8_weight",
-    "moe_fp8_init", "moe_fp8_destroy", "moe_fp8_sync_status", "moe_fp8_set_wait_limit_ns", "moe_add_rmsnorm_fp8",
-    "moe_fp8_matmul", "moe_fp8_gated_matmul", "moe_fp8_debug_plan",
+    "moe_fp8_init", "moe_fp8_destroy", "moe_fp8_sync_status", "moe_fp8_set_wait_limit_ns",
+    "moe_fp8_selftest_wait_timeout", "moe_add_rmsnorm_fp8", "moe_fp8_matmul", "moe_fp8_gated_matmul", "moe_fp8_debug_plan",
 ]
 
 MOE_BF16, MOE_FP16, MOE_FP32 = 0, 1, 2
@@ -49,6 +49,10 @@ def moe_fp8_sync_status(ctx, stream=None) -> int:
 
 def moe_fp8_set_wait_limit_ns(ctx, ns: int) -> None:
     _moe._check(_moe.lib().moe_fp8_set_wait_limit_ns(ctx, int(ns)), "moe_fp8_set_wait_limit_ns")
+
+
+def moe_fp8_selftest_wait_timeout(ctx, stream=None) -> None:
+    _moe._check(_moe.lib().moe_fp8_selftest_wait_timeout(ctx, _moe._stream(stream)), "moe_fp8_selftest_wait_timeout")
 
 
 def moe_add_rmsnorm_fp8(ctx, T, d, type, x, ldx, residual, ldr, norm_scale, eps, sum_out, lds, q, q_scale,
@@ -183,7 +187,9 @@ class Fp8Ops:
         return self._c.gated_matmul(self.ctx, self._index, a, a_scale, w13, w13_scale, bias, alpha, limit, shift)
 
     def sync_status(self, stream=None) -> int:
-        return moe_fp8_sync_status(self.ctx, stream)
+        """Waits for ``stream`` and returns MOE_OK, or MOE_ERR_TIMEOUT (once) where a device-side wait ran out."""
+        import torch
+        return moe_fp8_sync_status(self.ctx, torch.cuda.current_stream(self._index) if stream is None else stream)
 
 
 def _quantize(x, rows: int):

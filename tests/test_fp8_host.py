@@ -20,6 +20,7 @@ def test_null_context_and_null_results(lib):
     assert lib.moe_fp8_destroy(None) == moe.MOE_OK
     assert lib.moe_fp8_sync_status(None, None) == moe.MOE_ERR_ARG
     assert lib.moe_fp8_set_wait_limit_ns(None, 5) == moe.MOE_ERR_ARG
+    assert lib.moe_fp8_selftest_wait_timeout(None, None) == moe.MOE_ERR_ARG
     assert lib.moe_add_rmsnorm_fp8(None, 1, 64, 0, None, 64, None, 0, None, 1e-5, None, 0, None, None, None) == moe.MOE_ERR_ARG
     assert lib.moe_fp8_matmul(None, 1, 1, 16, None, 16, None, None, None, None, None, 0, None, 1, 0, None) == moe.MOE_ERR_ARG
     assert lib.moe_fp8_gated_matmul(None, 1, 16, 16, None, 16, None, None, None, None, 1.0, 7.0, 1.0, None, None, None) == moe.MOE_ERR_ARG
@@ -52,7 +53,7 @@ def test_sizes_types_strides_and_alignment(lib):
                                   v["ldr"], v["c"], v["ldc"], v["type"], None) == moe.MOE_ERR_ARG, b
     g = dict(M=4, F=32, K=64, a=P, lda=64, sa=P, b=P, sb=P, bias=None, alpha=1.0, limit=7.0, shift=1.0, h=P, hs=P)
     bad = [dict(F=0), dict(F=40), dict(K=24), dict(M=-2), dict(limit=0.0), dict(limit=-1.0), dict(limit=math.nan),
-           dict(alpha=math.nan), dict(shift=math.nan), dict(h=None), dict(h=P + 4), dict(hs=P + 2), dict(b=P + 4), dict(lda=56)]
+           dict(alpha=math.nan), dict(shift=math.nan), dict(alpha=math.inf), dict(shift=-math.inf), dict(h=None), dict(h=P + 4), dict(hs=P + 2), dict(b=P + 4), dict(lda=56)]
     for b in bad:
         v = {**g, **b}
         assert lib.moe_fp8_gated_matmul(c, v["M"], v["F"], v["K"], v["a"], v["lda"], v["sa"], v["b"], v["sb"], v["bias"],
@@ -86,6 +87,24 @@ def test_plans_fit_and_cover(lib, gated, M):
             else:
                 assert pl["grid"] % pl["ctas"] == 0 and pl["grid"] // pl["ctas"] <= pl["tiles"]
             assert not pl["few"] or M <= 16
+
+
+def test_gpu_sizes_cover_every_form(lib):
+    """The sizes of the GPU tests run every kernel: the one for a few rows, pairs, single tiles, split K (and, gated,
+    a split tile with one CTA), each with ragged rows and columns."""
+    import importlib.util
+    import os
+    spec = importlib.util.spec_from_file_location("gpu_fp8", os.path.join(os.path.dirname(__file__), "test_gpu_fp8.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+
+    def form(gated, size):
+        pl = moe.moe_fp8_debug_plan(gated, *size, 148)
+        return "few" if pl["few"] else "pair" if pl["ctas"] == 2 else "split" if pl["split"] > 1 else "single"
+
+    for gated, sizes in ((False, mod.SIZES), (False, mod.RES_SIZES), (True, mod.GATED_SIZES)):
+        forms = {form(gated, s) for s in sizes if s[0] % 128 and s[1] % 128}
+        assert forms == {"few", "pair", "single", "split"}, (gated, forms)
 
 
 def test_plan_rejects_bad_arguments(lib):

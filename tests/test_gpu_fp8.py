@@ -69,6 +69,16 @@ def test_norm_in_place_and_strided(ops):
         assert torch.equal(b[keep], base[keep])
 
 
+def test_norm_of_a_row_added_to_itself(ops):
+    """x as its own residual, and its sum in its place."""
+    x, w = randn(9, 400, seed=1, dtype=BF16), torch.ones(400, dtype=BF16, device="cuda")
+    want = ops.add_rmsnorm(x, w, residual=x.clone())
+    got = ops.add_rmsnorm(x, w, residual=x, sum_out=x)
+    assert got[2].data_ptr() == x.data_ptr()
+    for a, b in zip(got, want):
+        assert torch.equal(a.float(), b.float())
+
+
 def test_norm_zeros_infinities_and_nan(ops):
     """A row of zeros, and blocks of zeros, have the smallest scale and zero codes; a NaN spoils its own row
     only, an infinity makes its own block NaN and the rest of its row zero."""
@@ -93,7 +103,12 @@ def test_norm_zeros_infinities_and_nan(ops):
 
 SIZES = [(1, 1, 16), (1, 5, 32), (3, 16, 48), (8, 33, 128), (9, 31, 144), (32, 64, 256), (33, 65, 272), (64, 127, 400),
          (65, 129, 640), (127, 128, 1040), (128, 257, 128), (129, 255, 2064), (255, 130, 512), (257, 300, 784),
-         (1, 5120, 2880), (17, 2885, 2880), (300, 1000, 4112), (1000, 2880, 576), (2049, 1303, 304), (256, 5120, 2880), (200, 4901, 784)]
+         (1, 5120, 2880), (17, 2885, 2880), (300, 1000, 4112), (1000, 2880, 576), (2049, 1303, 304), (256, 5120, 2880), (200, 4901, 784),
+         (40, 19100, 144), (70, 20001, 272), (777, 5001, 400), (1100, 2885, 528)]
+RES_SIZES = [(1, 40, 64), (30, 2885, 272), (130, 257, 400), (513, 1024, 1552), (45, 19101, 144), (1100, 2885, 528), (300, 19000, 144)]
+GATED_SIZES = [(1, 16, 16), (2, 48, 64), (9, 128, 144), (32, 144, 256), (64, 272, 400), (65, 112, 128),
+               (128, 384, 1040), (129, 1360, 272), (257, 640, 528), (1, 2880, 2880), (31, 2880, 2880),
+               (1025, 2000, 304), (1030, 4112, 144), (100, 9600, 128), (150, 19104, 128)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -107,7 +122,7 @@ def test_matmul(ops, M, N, K, dtype):
     assert ((c.double() - want).abs() <= tol + (want.abs() + tol) * half_step(dtype) + 2.0 ** -25).all()
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (30, 2885, 272), (130, 257, 400), (513, 1024, 1552)])
+@pytest.mark.parametrize("M,N,K", RES_SIZES)
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 def test_matmul_bias_and_residual(ops, M, N, K, dtype):
     a, sa = rows(M, K, M)
@@ -213,9 +228,7 @@ def test_matmul_output_past_32_bits(ops):
 
 # ----------------------------------------------------------- the gated product
 
-@pytest.mark.parametrize("M,F,K", [(1, 16, 16), (2, 48, 64), (9, 128, 144), (32, 144, 256), (64, 272, 400), (65, 112, 128),
-                                   (128, 384, 1040), (129, 1360, 272), (257, 640, 528), (1, 2880, 2880), (31, 2880, 2880),
-                                   (1025, 2000, 304)])
+@pytest.mark.parametrize("M,F,K", GATED_SIZES)
 @pytest.mark.parametrize("act", sorted(ACTS))
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_gated(ops, M, F, K, act, with_bias):
@@ -355,6 +368,56 @@ def test_other_streams(ops):
             assert torch.equal(x, y)
         for x, y in zip(got_g, want_g):
             assert torch.equal(x[0].view(torch.uint8), y[0].view(torch.uint8)) and torch.equal(x[1], y[1])
+
+
+def test_wait_that_runs_out(ops):
+    """The status reports it once; the object stays usable."""
+    ops2 = moe.Fp8Ops()
+    moe.moe_fp8_set_wait_limit_ns(ops2.ctx, 2_000_000)
+    moe.moe_fp8_selftest_wait_timeout(ops2.ctx)
+    assert ops2.sync_status() == moe.MOE_ERR_TIMEOUT
+    assert ops2.sync_status() == moe.MOE_OK
+    moe.moe_fp8_set_wait_limit_ns(ops2.ctx, 2_000_000_000)
+    for M in (1, 40, 600):
+        a, b = rows(M, 272, 1), weight(300, 272, 2)
+        assert torch.equal(ops2.matmul(*a, *b), ops.matmul(*a, *b))
+    assert ops2.sync_status() == moe.MOE_OK
+    ops2.close()
+
+
+CAPTURE_FIRST = """
+import sys, torch
+sys.path[:0] = [%r, %r]
+import sparse_moe_rmsnorm_b200 as moe
+from _fp8 import rows, weight
+ops = moe.Fp8Ops()
+w = torch.ones(272, dtype=torch.bfloat16, device="cuda")
+data = [(rows(M, 272, M), weight(N, 272, N), torch.randn(M, 272, device="cuda").bfloat16()) for M, N in ((1, 300), (40, 300), (600, 5000))]
+gs = [torch.stack([weight(N // 32 * 16, 272, 3)[1]] * 2) for N in (300, 300, 5000)]
+g = torch.cuda.CUDAGraph()
+def call():
+    return [(ops.matmul(*a, *b), *ops.gated_matmul(*a, b[0][:b[0].shape[0] // 32 * 32], s), *ops.add_rmsnorm(x, w, residual=x))
+            for (a, b, x), s in zip(data, gs)]
+with torch.cuda.graph(g):
+    out = call()
+g.replay()
+torch.cuda.synchronize()
+for one, other in zip(out, call()):
+    for p, q in zip(one, other):
+        assert torch.equal(p.float(), q.float())
+assert ops.sync_status() == moe.MOE_OK
+print("captured first")
+"""
+
+
+def test_first_calls_captured():
+    """A process whose first calls, of every form, are inside a capture."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST % (os.path.dirname(here), here)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
 def test_empty_batches(ops):
