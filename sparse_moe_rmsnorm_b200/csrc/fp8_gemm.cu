@@ -275,7 +275,7 @@ template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr int WGS = FP8_WGS;                // epilogue warpgroups
     constexpr int CW = BN / WGS;                // accumulator columns per epilogue thread
-    constexpr int LD = CW > 64 && !GATED ? 32 : 16;     // columns of a TMEM load (registers: 2 LD beside the CW sums)
+    constexpr int LD = CW > 64 && !GATED && !RES ? 32 : 16;     // columns of a TMEM load (registers: 2 LD beside the CW sums)
     constexpr int CC = FP8_TILE_COLS;           // columns of a staging tile
     constexpr int HW = CW / 2;                  // gated: h columns per thread
     constexpr int BUFS = fp8_bufs(BN);
@@ -285,7 +285,9 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
     static_assert(!GATED || HW * WGS == FP8_BLOCK, "the warpgroups share a gated row's block");
     static_assert(!SK || CTAS == 1, "CTAs of a cluster split K, or are a pair");
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // 1024-aligned, as an offset from the array: a pointer rounded as a number is no longer known to be shared
+    // memory, and its loads and stores become generic ones
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const int NS = p.n_stages;
     const Fp8Smem plan = fp8_smem(BN, CTAS, GATED, SK, p.a_rows, NS);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + plan.bar_off);

@@ -48,37 +48,45 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// One try_wait, which may sleep in the barrier unit for a time the hardware sets.  (With a time hint it is a
+// loop with clock reads and sleeps of its own, and takes longer also where the phase is complete.)
 template <bool CLUSTER>
-__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     if constexpr (CLUSTER)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(hint_ns)
+            : "r"(bar), "r"(parity)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(hint_ns)
+            : "r"(bar), "r"(parity)
             : "memory");
     return ok != 0;
 }
 
-// The rest of a wait whose first sleep in the barrier unit has ended without the phase.
+// A bounded wait as mbar_wait, by any thread: the limit is looked at after every 64 tries, its start taken after
+// the first 64, so an ordinary wait reads no timer.  False where it ran out or the CTA has aborted.  CLUSTER: other
+// CTAs arrive on the barrier; acquires at cluster scope.
 template <bool CLUSTER>
-__device__ __forceinline__ bool wait_phase_long(uint32_t bar, uint32_t parity, const WaitCtl &w) {
-    const uint64_t start = globaltimer_ns();
-    for (;;) {
-        if (try_phase<CLUSTER>(bar, parity, MBAR_SUSPEND_HINT_NS)) return true;
-        if (*w.abort) return false;
-        if (globaltimer_ns() - start > w.limit_ns) {
-            *w.abort = 1;
-            atomicOr(w.err, w.err_bit);
-            return false;
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const WaitCtl &w) {
+    uint32_t start = 0;                     // in 1024 ns
+    for (uint32_t i = 1;; ++i) {
+        if (try_phase<CLUSTER>(bar, parity)) return true;
+        if (i % 64 == 0) {
+            const uint32_t now = (uint32_t)(globaltimer_ns() >> 10);
+            if (i == 64) start = now;
+            if (*w.abort) return false;
+            if (now - start > (w.limit_ns >> 10)) {
+                *w.abort = 1;
+                atomicOr(w.err, w.err_bit);
+                return false;
+            }
         }
     }
 }
@@ -86,16 +94,8 @@ __device__ __forceinline__ bool wait_phase_long(uint32_t bar, uint32_t parity, c
 // wait_phase for the lanes of a warp that stays converged: a wait that runs out sets the abort flag and
 // returns like any other; the warp looks at the flag where it can leave together.
 __device__ __forceinline__ void wait_phase_through(uint32_t bar, uint32_t parity, const WaitCtl &w) {
-    if (!try_phase<false>(bar, parity, MBAR_SUSPEND_HINT_NS)) wait_phase_long<false>(bar, parity, w);
+    wait_phase<false>(bar, parity, w);
     __syncwarp();
-}
-
-// Bounded wait as mbar_wait, by any thread.  The limit's start is taken after the first sleep (1 ms), so
-// an ordinary wait reads no timer.  CLUSTER: other CTAs arrive on the barrier; acquires at cluster scope.
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const WaitCtl &w) {
-    if (try_phase<CLUSTER>(bar, parity, MBAR_SUSPEND_HINT_NS)) return true;
-    return wait_phase_long<CLUSTER>(bar, parity, w);
 }
 
 // --------------------------------------------------------------------- TMA
