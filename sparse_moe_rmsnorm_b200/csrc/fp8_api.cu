@@ -263,7 +263,7 @@ int moe_fp8_matmul(moe_fp8_ctx_t *c, int M, int N, int K, const uint8_t *a, int6
     p.c = out;
     p.ldc = ldc;
     p.type = type;
-    p.vec = aligned(out, 16) && ldc * eb % 16 == 0 && (!residual || (aligned(residual, 16) && ldr * eb % 16 == 0));
+    p.vec = aligned(out, 4 * eb) && ldc % 4 == 0 && (!residual || (aligned(residual, 4 * eb) && ldr % 4 == 0));
     return status(launch_fp8_gemm(p, pl, 0, static_cast<cudaStream_t>(stream)));
 }
 

@@ -56,18 +56,19 @@ __device__ __forceinline__ float gated_value(const Fp8GemmParams &p, float g, fl
     return g * rcp_approx(1.0f + exp2_approx(p.minus_alpha_log2e * g)) * (u + p.shift);
 }
 
-// V elements (1 or 4) of type T.
+// V elements (1, 2 or 4) of type T.
 template <typename T, int V>
 struct Pack {
-    typename std::conditional<V == 1, T, typename std::conditional<sizeof(T) == 4, uint4, uint2>::type>::type raw;
+    typename std::conditional<V * sizeof(T) == 16, uint4, typename std::conditional<V * sizeof(T) == 8, uint2,
+        typename std::conditional<V == 2, uint32_t, T>::type>::type>::type raw;
     __device__ __forceinline__ float get(int j) const { return static_cast<float>(reinterpret_cast<const T *>(&raw)[j]); }
     __device__ __forceinline__ void set(const float (&v)[V]) {
-        if constexpr (V == 4 && std::is_same<T, __half>::value) {
-            reinterpret_cast<__half2 *>(&raw)[0] = __floats2half2_rn(v[0], v[1]);
-            reinterpret_cast<__half2 *>(&raw)[1] = __floats2half2_rn(v[2], v[3]);
-        } else if constexpr (V == 4 && std::is_same<T, __nv_bfloat16>::value) {
-            reinterpret_cast<__nv_bfloat162 *>(&raw)[0] = __floats2bfloat162_rn(v[0], v[1]);
-            reinterpret_cast<__nv_bfloat162 *>(&raw)[1] = __floats2bfloat162_rn(v[2], v[3]);
+        if constexpr (V > 1 && std::is_same<T, __half>::value) {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) reinterpret_cast<__half2 *>(&raw)[j] = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        } else if constexpr (V > 1 && std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) reinterpret_cast<__nv_bfloat162 *>(&raw)[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) reinterpret_cast<T *>(&raw)[j] = static_cast<T>(v[j]);
@@ -123,9 +124,80 @@ __device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *ti
     }
 }
 
+// The same for 16-bit types where rows start anywhere or end inside the tile.  16 lanes take a row, each two
+// neighbours that share a word of c: columns 2 i and 2 i + 1, or, where the row starts inside a word, 1 + 2 i and
+// 2 + 2 i (a lane's rows are two apart, so they start alike).  What is left at a row's ends, one column each, is
+// written a lane a row.  (An element a lane: twice the loads and stores.  The residual's are asm so that they stay
+// in one stream: as branches, each waited for its own.)
+template <typename T, int CC, bool RES>
+__device__ __forceinline__ void put_pairs(const Fp8GemmParams &p, const float *tile, float bias, int m0, int n0, int lane) {
+    static_assert(CC == 32 && sizeof(T) == 2, "a row is 16 lanes' words");
+    constexpr int B = RES ? 8 : 4;              // steps at a time
+    const int rows = min(32, p.M - m0), cols = min(CC, p.N - n0);
+    const auto half = [](const T *at) { return (int)(reinterpret_cast<uintptr_t>(at) >> 1 & 1); };
+    T *c = static_cast<T *>(p.c) + (long long)m0 * p.ldc + n0;
+    const T *res = RES ? static_cast<const T *>(p.residual) + (long long)m0 * p.ldr + n0 : nullptr;
+
+    T *end_c = c + lane * p.ldc;
+    const T *end_res = RES ? res + lane * p.ldr : nullptr;
+    const int lead = half(end_c);
+    const bool end0 = lane < rows && lead, end1 = lane < rows && ((cols - lead) & 1);
+    uint32_t old0 = 0, old1 = 0;
+    if constexpr (RES) {
+        ld_u16_if(old0, end_res, end0);
+        ld_u16_if(old1, end_res + (cols - 1), end1);
+    }
+
+    const int r0 = lane >> 4;
+    c += r0 * p.ldc;
+    const int k = 2 * (lane & 15) + half(c);
+    const float b0 = __shfl_sync(0xffffffffu, bias, k), b1 = __shfl_sync(0xffffffffu, bias, (k + 1) & 31);
+    const bool in = k + 1 < cols;
+    c += k;
+    if (RES) res += r0 * p.ldr + k;
+    const bool apart = RES && half(res);        // the residual's rows start otherwise than c's
+    const float *f = tile + r0 * (CC + 4) + k;
+#pragma unroll 1
+    for (int r = r0; r < rows; r += 2 * B) {
+        uint32_t lo[B], hi[B];
+        if constexpr (RES) {
+#pragma unroll
+            for (int i = 0; i < B; ++i, res += 2 * p.ldr) {
+                const bool on = in && r + 2 * i < rows;
+                hi[i] = 0;
+                ld_u32_if(lo[i], res, on && !apart);
+                ld_u16_if(lo[i], res, on && apart);
+                ld_u16_if(hi[i], res + 1, on && apart);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i, c += 2 * p.ldc, f += 2 * (CC + 4)) {
+            if (in && r + 2 * i < rows) {
+                float o[2] = {f[0] + b0, f[1] + b1};
+                if constexpr (RES) {
+                    Pack<T, 2> old;
+                    old.raw = lo[i] | hi[i] << 16;
+                    o[0] += old.get(0), o[1] += old.get(1);
+                }
+                Pack<T, 2> out;
+                out.set(o);
+                *reinterpret_cast<uint32_t *>(c) = out.raw;
+            }
+        }
+    }
+
+    const float be = __shfl_sync(0xffffffffu, bias, cols - 1), bl = __shfl_sync(0xffffffffu, bias, 0);
+    f = tile + lane * (CC + 4);
+    Pack<T, 2> old;
+    old.raw = old0 | old1 << 16;
+    if (end0) *end_c = static_cast<T>(f[0] + bl + (RES ? old.get(0) : 0.0f));
+    if (end1) end_c[cols - 1] = static_cast<T>(f[cols - 1] + be + (RES ? old.get(1) : 0.0f));
+}
+
 template <typename T, int CC, bool RES>
 __device__ __forceinline__ void put_tile(const Fp8GemmParams &p, const float *tile, float bias, int m0, int n0, int lane) {
     if (p.vec && m0 + 32 <= p.M && n0 + CC <= p.N) put_tile<T, CC, 4, RES>(p, tile, bias, m0, n0, lane);
+    else if constexpr (sizeof(T) == 2) put_pairs<T, CC, RES>(p, tile, bias, m0, n0, lane);
     else put_tile<T, CC, 1, RES>(p, tile, bias, m0, n0, lane);
 }
 

@@ -40,7 +40,7 @@ struct Fp8GemmParams {
     void *c;                        // type [M, N], rows ldc elements apart
     long long ldr, ldc;
     int type;                       // FP8_BF16, FP8_FP16 or FP8_FP32
-    int vec;                        // rows of c (and of the residual) start on 16 bytes
+    int vec;                        // rows of c (and of the residual) start on four elements
     float minus_alpha_log2e, limit, shift;      // gated activation
     uint8_t *h;                     // gated: E4M3 [M, F]
     float *h_scale;                 // gated: [M, NB]

@@ -207,6 +207,14 @@ __device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
+// Loads that a predicate turns off (v keeps its value), in program order among themselves.
+__device__ __forceinline__ void ld_u32_if(uint32_t &v, const void *at, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((uint32_t)on) : "memory");
+}
+__device__ __forceinline__ void ld_u16_if(uint32_t &v, const void *at, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u16 %0, [%1];\n\t}" : "+r"(v) : "l"(at), "r"((uint32_t)on) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Four bytes from global to shared memory, asynchronously.

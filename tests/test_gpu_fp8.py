@@ -166,6 +166,44 @@ def test_matmul_strides_leave_the_rest(ops, M, N, dtype):
         assert (cbuf[keep] == 7).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 19000, 144), (70, 19101, 144), (37, 2886, 272)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("c_at,c_pad,r_at,r_pad", [(0, 1, 0, 1), (1, 0, 1, 0), (1, 3, 1, 2), (2, 2, 1, 4), (3, 1, 0, 4), (4, 4, 4, 8)])
+def test_matmul_rows_that_start_anywhere(ops, M, N, K, dtype, c_at, c_pad, r_at, r_pad):
+    """Every element comes out the same wherever the rows of the result and of the residual start, and what lies
+    around them stays; in place of the residual too."""
+    a, sa = rows(M, K, M)
+    b, sb = weight(N, K, N)
+    bias, res = randn(N, seed=3, dtype=BF16), randn(M, N, seed=4, dtype=dtype)
+    plain, want = (ops.matmul(a, sa, b, sb, bias=bias, residual=r, out_dtype=dtype) for r in (None, res))
+    exact, tol = product_ref(a, sa, b, sb)
+    for more in (bias, res):
+        exact = exact + more.double()
+        tol = tol + (exact.abs() + tol) * U32
+    assert ((want.double() - exact).abs() <= tol + (exact.abs() + tol) * half_step(dtype) + 2.0 ** -25).all()
+
+    def lain(at, pad, fill):
+        base = torch.full((at + M * (N + pad) + 7,), -77.0, dtype=dtype, device="cuda")
+        view = base[at:at + M * (N + pad)].view(M, N + pad)[:, :N]
+        if fill is not None:
+            view.copy_(fill)
+        return base, view
+
+    for same in (False, True):
+        r_base, r = lain(c_at if same else r_at, c_pad if same else r_pad, res)
+        c_base, c = (r_base, r) if same else lain(c_at, c_pad, None)
+        ops.matmul(a, sa, b, sb, bias=bias, residual=r, out=c)
+        assert torch.equal(c, want)
+        c.fill_(-77.0)
+        assert (c_base == -77.0).all()
+        if not same:
+            assert torch.equal(r, res)
+            ops.matmul(a, sa, b, sb, bias=bias, out=c)
+            assert torch.equal(c, plain)
+            c.fill_(-77.0)
+            assert (c_base == -77.0).all()
+
+
 def test_matmul_padded_batch_leaves_rows_behind(ops):
     """A batch of 70 rows in a buffer of 200: the rows behind stay, whatever the operand holds there."""
     M, N, K = 70, 300, 528
