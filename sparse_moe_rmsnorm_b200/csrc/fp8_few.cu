@@ -4,14 +4,19 @@
 // the time is their way from memory (and, for one token, mostly the launch).  The tensor-memory kernel
 // spends some 300 cycles per 128-K block on its hand-overs (copy, MMA, scaled sums); a chain of 23
 // blocks then takes longer than the weights' copy.  So here every warp is on its own: it loads its
-// weights from global memory straight into the operands of mma.sync m16n8k32 (weights the 16 rows,
-// tokens the 8 columns), scales each K block's sums in registers, and the CTA's eight warps, which split
+// weights from global memory straight into the operands of mma.sync m16n8k16 (weights the 16 rows,
+// tokens the 8 columns; E4M3 to f16 is exact, and two conversions and an f16 product took less than the E4M3
+// form of mma.sync), scales each K block's sums in registers, and the CTA's eight warps, which split
 // K, add up at the end in a fixed order.
 //
+// One token, in a run of calls: 5120 x 2880 in 4.6 us (14.8 MB, 3.2 TB/s; 10.2 in the other kernel), gated
+// 2 x 2880 x 2880 in 6.2 us (16.6 MB, 2.7 TB/s; 11.8): latency, of the launch, of one round of loads (eight
+// of ten samples of a warp wait for memory) and of the join, and for the gated form of the cluster's exchange.
+//
 // Operands without shuffles: the K order within a product is free as long as both sides use the
-// same.  Lane (g, t) takes the 16 bytes t of a 64-byte K segment of rows g and g + 8 (of token g): their
-// words 0 and 1 are one MMA's a0, a2 (b0, b1), words 2 and 3 the next one's.  So every load is 16
-// bytes wide and four lanes take 64 contiguous bytes.
+// same.  Lane (g, t) takes the 16 bytes t of a 64-byte K segment of rows g and g + 8 (of token g); each of their
+// words, as two f16 pairs, is one MMA's a0, a2 (a1, a3; b0, b1).  So every load is 16 bytes wide and four lanes
+// take 64 contiguous bytes.
 //
 // Gated: a CTA takes 16 gate rows and their 16 linear rows; a row's 128-column block of h lies in a
 // cluster of eight CTAs, which exchange its maximum through distributed shared memory.

@@ -6,8 +6,8 @@
 // The norm is the routed block's (no bias, no mean subtraction: pnsm.cn overview, section 2.3;
 // "gpt-oss-20B" hub page, section 3.2) and stands beside it: here the rows leave in the form the
 // dense 8-bit products read.  Bound by HBM: x, r, the sum and q move once (8192 rows of 2880, bf16:
-// 166 MB in 28.0 us, 0.90 of the measured copy rate), and next by instruction issue: the arithmetic is on
-// pairs (f32x2), which took it from 39 us.  One CTA holds a row in registers, 8 or 16 elements per
+// 166 MB in 28.8 us alone and 30.0 in a run of calls, 0.88 and 0.84 of the measured copy rate), and next by
+// instruction issue (75% of the slots): the arithmetic is on pairs (f32x2), which took it from 39 us.  One CTA holds a row in registers, 8 or 16 elements per
 // thread, so the row is read once and the second pass (the scaling) needs no memory; a block's 128
 // elements sit in 16 neighbouring lanes, so its maximum is four shuffles.  A row's sum adds the
 // elements of a thread in two halves, then a tree over lanes and warps.
