@@ -268,8 +268,7 @@ MOE_API int moe_forward_noalloc(int T, int d_model, int d_ff, int n_experts, int
  * No call allocates or keeps anything: there is no workspace, and calls on one
  * context may overlap (streams, host threads, captured graphs).  Results do not
  * depend on timing: the same inputs give the same bits.  Rows, columns and K are
- * at most 2^30.  Outputs must not
- * overlap inputs except where stated.  The context's device is made current
+ * at most 2^30.  Outputs must not overlap inputs except where stated.  The context's device is made current
  * during a call; pointers and stream belong to it. */
 
 enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 };   /* types of x, residual, sum and c */
@@ -302,7 +301,7 @@ MOE_API int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *ctx, int T, int d, int type, cons
  * a u8 [M, K], rows lda bytes apart (multiple of 16); b u8 [N, K]; K a multiple of 16;
  * bias bf16 [N] or NULL; c, residual: type [M, N], rows ldc / ldr elements apart;
  * residual may be NULL, or c itself.  a and b 16-byte aligned, c and residual to their
- * type (rows on 16-byte units are the fast case). */
+ * type (rows that start on four elements are the fast case). */
 MOE_API int moe_fp8_matmul(moe_fp8_ctx_t *ctx, int M, int N, int K, const uint8_t *a, int64_t lda,
                    const float *a_scale, const uint8_t *b, const float *b_scale, const uint16_t *bias,
                    const void *residual, int64_t ldr, void *c, int64_t ldc, int type, void *stream);
@@ -311,8 +310,8 @@ MOE_API int moe_fp8_matmul(moe_fp8_ctx_t *ctx, int M, int N, int K, const uint8_
  *   g = min(W13_gate a + b_gate, limit),  u = clamp(W13_linear a + b_linear, -limit, limit),
  *   h = g * sigmoid(alpha g) * (u + shift), then E4M3 with a scale per 128 columns.
  * (alpha, limit, shift) = (1.702, 7, 1) is the experts' activation, (1, INFINITY, 0) is
- * silu(gate) * linear; alpha and shift are finite, limit > 0.  a, a_scale as above; w13 u8 [2, F, K] (gate rows, then linear rows),
- * w13_scale fp32 [2, ceil(F/128), ceil(K/128)] (each half has its own blocks), b13 bf16
+ * silu(gate) * linear; alpha and shift are finite, limit > 0.  a, a_scale as above;
+ * w13 u8 [2, F, K] (gate rows, then linear rows), w13_scale fp32 [2, ceil(F/128), ceil(K/128)] (each half has its own blocks), b13 bf16
  * [2, F] or NULL; h u8 [M, F], h_scale fp32 [M, ceil(F/128)].  F a multiple of 16. */
 MOE_API int moe_fp8_gated_matmul(moe_fp8_ctx_t *ctx, int M, int F, int K, const uint8_t *a, int64_t lda,
                          const float *a_scale, const uint8_t *w13, const float *w13_scale, const uint16_t *b13,

@@ -102,6 +102,8 @@ bool same_place(const Tensor &a, const Tensor &b) {
 template <typename T>
 T *ptr(const Tensor &t) { return static_cast<T *>(const_cast<void *>(t.const_data_ptr())); }
 template <typename T>
+T *ptr_to_write(const Tensor &t) { return static_cast<T *>(t.mutable_data_ptr()); }
+template <typename T>
 T *ptr(const OptTensor &t) { return t ? ptr<T>(*t) : nullptr; }
 
 moe_fp8_ctx_t *ctx_of(uintptr_t c) { return reinterpret_cast<moe_fp8_ctx_t *>(c); }
@@ -130,7 +132,8 @@ py::tuple add_rmsnorm(uintptr_t ctx, int device, const Tensor &x, const Tensor &
     Tensor q = c.empty({T, d}, at::kFloat8_e4m3fn), s = c.empty({T, blocks(d)}, at::kFloat);
     c.done(moe_add_rmsnorm_fp8(ctx_of(ctx), c.size(T, "rows"), c.size(d, "columns"), code, x.const_data_ptr(), ldx,
                                ptr<void>(residual), ldr, ptr<uint16_t>(norm_scale), (float)eps,
-                               residual ? ptr<void>(sum) : nullptr, lds, ptr<uint8_t>(q), ptr<float>(s), c.stream()));
+                               residual ? ptr_to_write<void>(sum) : nullptr, lds, ptr_to_write<uint8_t>(q), ptr_to_write<float>(s),
+                               c.stream()));
     return residual ? py::make_tuple(q, s, sum) : py::make_tuple(q, s);
 }
 
@@ -159,7 +162,7 @@ Tensor matmul(uintptr_t ctx, int device, const Tensor &a, const Tensor &a_scale,
     Tensor y = out ? *out : c.empty({M, N}, t);
     c.done(moe_fp8_matmul(ctx_of(ctx), c.size(M, "rows"), c.size(N, "columns"), c.size(K, "elements"), ptr<uint8_t>(a), lda,
                           ptr<float>(a_scale), ptr<uint8_t>(b), ptr<float>(b_scale), ptr<uint16_t>(bias),
-                          ptr<void>(residual), ldr, ptr<void>(y), ldc, code, c.stream()));
+                          ptr<void>(residual), ldr, ptr_to_write<void>(y), ldc, code, c.stream()));
     return y;
 }
 
@@ -176,8 +179,8 @@ py::tuple gated_matmul(uintptr_t ctx, int device, const Tensor &a, const Tensor 
     Tensor h = c.empty({M, F}, at::kFloat8_e4m3fn), s = c.empty({M, blocks(F)}, at::kFloat);
     c.done(moe_fp8_gated_matmul(ctx_of(ctx), c.size(M, "rows"), c.size(F, "columns"), c.size(K, "elements"),
                                 ptr<uint8_t>(a), lda, ptr<float>(a_scale), ptr<uint8_t>(w13), ptr<float>(w13_scale),
-                                ptr<uint16_t>(bias), (float)alpha, (float)limit, (float)shift, ptr<uint8_t>(h),
-                                ptr<float>(s), c.stream()));
+                                ptr<uint16_t>(bias), (float)alpha, (float)limit, (float)shift,
+                                ptr_to_write<uint8_t>(h), ptr_to_write<float>(s), c.stream()));
     return py::make_tuple(h, s);
 }
 

@@ -144,6 +144,8 @@ class Fp8Ops:
         import torch
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
+        if stream.device != self.device:        # the device's own current stream would be taken in its place
+            raise _moe.MoEError(_moe.MOE_ERR_ARG, f"stream of {stream.device}, operators of {self.device}")
         return torch.cuda.stream(stream)
 
     def add_rmsnorm(self, x, norm_scale, residual=None, eps: float = 1e-5, sum_out=None, stream=None):

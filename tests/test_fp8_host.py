@@ -129,3 +129,12 @@ def test_quantisers(M, K):
                 v = q[i * rows:(i + 1) * rows, 128 * j:128 * (j + 1)].double() * s[i, j].double()
                 assert abs(s[i, j].double() - max(b.abs().max() / 448, 2.0 ** -126)) <= 2.0 ** -23 * s[i, j].double()
                 assert ((v - b).abs() <= b.abs() * (2.0 ** -4 + 2.0 ** -22) + s[i, j].double() * 2.0 ** -10).all()
+
+
+def test_stream_of_another_device_is_refused():
+    """Its calls would run on the operators' device's current stream instead."""
+    import types
+    ops = object.__new__(moe.Fp8Ops)
+    ops.device, ops.ctx = torch.device("cuda", 0), None
+    with pytest.raises(moe.MoEError):
+        ops._on(types.SimpleNamespace(device=torch.device("cuda", 1)))
