@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
             int slot = skip % NS, buf = skip % BUFS;
             uint32_t ph = 0, dph = 0;
             bool ok = true, any = false;
+            pdl_wait();                                 // (it reads no such memory, but its waits' time starts here)
             for (long long g = skip; g < blocks; g += BY) {
                 if (!wait_phase<CTAS == 2>(d_empty0 + 8u * buf, dph ^ 1, wc) || !wait_phase<false>(full0 + 8u * slot, ph, wc)) {
                     ok = false;

@@ -423,6 +423,36 @@ def test_wait_that_runs_out(ops):
     ops2.close()
 
 
+def test_waits_do_not_count_the_kernel_before():
+    """A product of few tiles and a very long K lasts longer than the limit of a single wait; the next product, which
+    has SMs to start on meanwhile, waits for it without running out."""
+    ops2, limit_ns = moe.Fp8Ops(), 1_000_000
+    M, N, K = 17, 16, 1 << 24
+    a, sa = torch.zeros(M, K, dtype=torch.uint8, device="cuda"), torch.ones(M, K // 128, device="cuda")
+    b, sb = torch.zeros(N, K, dtype=torch.uint8, device="cuda"), torch.ones(1, K // 128, device="cuda")
+    data = [((M, K), (N, K)) for M, N, K in ((40, 300, 272), (600, 5000, 272), (70, 19101, 144))]
+    data = [(rows(*ra, 1), weight(*rb, 2)) for ra, rb in data]
+    want = [ops2.matmul(*x, *w) for x, w in data]
+    long_out = torch.empty(M, N, dtype=BF16, device="cuda")
+    ops2.matmul(a, sa, b, sb, out=long_out)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    ops2.matmul(a, sa, b, sb, out=long_out)
+    end.record()
+    torch.cuda.synchronize()
+    assert start.elapsed_time(end) * 1e6 > 2 * limit_ns         # (or the test shows nothing)
+    assert ops2.sync_status() == moe.MOE_OK
+    moe.moe_fp8_set_wait_limit_ns(ops2.ctx, limit_ns)
+    for (x, w), y in zip(data, want):
+        out = torch.empty_like(y)
+        torch.cuda.synchronize()
+        ops2.matmul(a, sa, b, sb, out=long_out)
+        ops2.matmul(*x, *w, out=out)
+        assert ops2.sync_status() == moe.MOE_OK
+        assert torch.equal(out, y) and (long_out == 0).all()
+    ops2.close()
+
+
 CAPTURE_FIRST = """
 import sys, torch
 sys.path[:0] = [%r, %r]
