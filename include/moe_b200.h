@@ -280,8 +280,9 @@ typedef struct moe_fp8_ctx moe_fp8_ctx_t;
 MOE_API int moe_fp8_init(moe_fp8_ctx_t **out);
 MOE_API int moe_fp8_destroy(moe_fp8_ctx_t *ctx);
 
-/* As moe_sync_status, moe_set_wait_limit_ns and moe_selftest_wait_timeout.  (A context's
- * calls may be captured from the first on; the status is asked for outside a capture.) */
+/* As moe_sync_status, moe_set_wait_limit_ns (a millisecond at least, else MOE_ERR_ARG) and
+ * moe_selftest_wait_timeout.  (A context's calls may be captured from the first on; the status
+ * is asked for outside a capture.) */
 MOE_API int moe_fp8_sync_status(moe_fp8_ctx_t *ctx, void *stream);
 MOE_API int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *ctx, unsigned long long ns);
 MOE_API int moe_fp8_selftest_wait_timeout(moe_fp8_ctx_t *ctx, void *stream);

@@ -190,7 +190,7 @@ int moe_fp8_sync_status(moe_fp8_ctx_t *c, void *stream) {
 }
 
 int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *c, unsigned long long ns) {
-    if (!c || ns == 0) return MOE_ERR_ARG;
+    if (!c || ns < FP8_WAIT_LIMIT_MIN_NS) return MOE_ERR_ARG;
     c->wait_limit_ns = ns;
     return MOE_OK;
 }

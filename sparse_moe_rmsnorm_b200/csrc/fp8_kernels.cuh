@@ -79,6 +79,10 @@ struct Fp8Plan {
     int m_tiles, tiles, grid;
 };
 
+// The shortest limit of a wait.  A CTA that gives up waits as long again for its copies and MMAs in flight before it
+// frees TMEM and leaves; they take microseconds, so from here on they have landed by then, its pair's too.
+constexpr unsigned long long FP8_WAIT_LIMIT_MIN_NS = 1000000;
+
 constexpr int FP8_SIZE_MAX = 1 << 30;   // rows, columns and K, at most
 constexpr int FP8_BM = 128;             // rows of A per CTA (TMEM lanes)
 constexpr int FP8_KS = 128;             // K elements per stage: one scale block

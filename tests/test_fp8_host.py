@@ -64,6 +64,18 @@ def test_sizes_types_strides_and_alignment(lib):
     assert lib.moe_fp8_gated_matmul(c, 0, 32, 64, None, 0, None, None, None, None, 1.0, 7.0, 1.0, None, None, None) == moe.MOE_OK
 
 
+def test_wait_limits_shorter_than_a_drain_are_refused(lib):
+    """A CTA whose wait ran out waits as long again for its copies in flight: a limit of microseconds would let it
+    leave before they land."""
+    c = Ctx(0, 148, None, 2_000_000_000)
+    for ns in (0, 1, 1000, 999_999):
+        assert lib.moe_fp8_set_wait_limit_ns(ctypes.byref(c), ns) == moe.MOE_ERR_ARG
+        assert c.limit == 2_000_000_000
+    for ns in (1_000_000, 2_000_000, 1 << 62):
+        assert lib.moe_fp8_set_wait_limit_ns(ctypes.byref(c), ns) == moe.MOE_OK
+        assert c.limit == ns
+
+
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("M", [1, 7, 8, 9, 32, 64, 65, 128, 129, 255, 333, 1000, 2048, 8192, 100000])
 def test_plans_fit_and_cover(lib, gated, M):
