@@ -275,15 +275,19 @@ enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_FP32 = 2 };   /* types of x, residual, su
 
 typedef struct moe_fp8_ctx moe_fp8_ctx_t;
 
-/* Create a context on the current device: its SM count and the latched error
- * word of the bounded waits.  Call it outside stream captures. */
+/* Create a context on the current device: its SM count and the count of bounded
+ * waits that ran out.  Call it outside stream captures. */
 MOE_API int moe_fp8_init(moe_fp8_ctx_t **out);
 MOE_API int moe_fp8_destroy(moe_fp8_ctx_t *ctx);
 
-/* As moe_sync_status, moe_set_wait_limit_ns (a millisecond at least, else MOE_ERR_ARG) and
- * moe_selftest_wait_timeout.  (A context's calls may be captured from the first on; the status
- * is asked for outside a capture.) */
+/* Synchronise `stream`; MOE_ERR_TIMEOUT where a wait of any call on this context ran out since
+ * `stream` last asked (a stream that asks for the first time: since moe_fp8_init), else MOE_OK.
+ * So each stream hears of a timeout once, whichever asks first; whose it was the context does not
+ * know, and streams that want to know take a context each.  (A context's calls may be captured
+ * from the first on; the status is asked for outside a capture, on the stream of the replays.) */
 MOE_API int moe_fp8_sync_status(moe_fp8_ctx_t *ctx, void *stream);
+
+/* As moe_set_wait_limit_ns (a millisecond at least, else MOE_ERR_ARG) and moe_selftest_wait_timeout. */
 MOE_API int moe_fp8_set_wait_limit_ns(moe_fp8_ctx_t *ctx, unsigned long long ns);
 MOE_API int moe_fp8_selftest_wait_timeout(moe_fp8_ctx_t *ctx, void *stream);
 

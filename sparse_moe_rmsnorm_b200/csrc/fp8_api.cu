@@ -5,6 +5,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <map>
+#include <mutex>
 #include <new>
 
 #include "moe_b200.h"
@@ -16,21 +18,24 @@ cudaError_t launch_add_rmsnorm_fp8(const Fp8NormParams &p, int type, int num_sms
 cudaError_t fp8_gemm_setup(int *clusters);
 cudaError_t fp8_few_setup();
 cudaError_t fp8_norm_setup();
-cudaError_t launch_selftest_wait(unsigned int *err, unsigned long long limit_ns, cudaStream_t s);
+cudaError_t launch_fp8_selftest_wait(unsigned int *err, unsigned long long limit_ns, cudaStream_t s);
 cudaError_t launch_fp8_few(const Fp8FewParams &p, int gated, cudaStream_t s);
 cudaError_t launch_fp8_gemm(const Fp8GemmParams &p, const Fp8Plan &pl, int gated, cudaStream_t s);
 }  // namespace moe
 
 using namespace moe;
 
-// Nothing but the latched error word lives on the device, so calls on one context from several
-// streams, host threads or captured graphs share no workspace.
+// Nothing but the count of waits that ran out lives on the device, so calls on one context from several
+// streams, host threads or captured graphs share no workspace.  The count only grows: a stream that asks for the
+// status hears whether it grew since that stream asked last, and takes nothing from another's answer.
 struct moe_fp8_ctx {
     int device;
     int num_sms;
     unsigned int *err;
     unsigned long long wait_limit_ns;
     int clusters[FP8_SPLIT_MAX + 1];    // clusters of n CTAs that the device holds at once
+    std::mutex lock;
+    std::map<unsigned long long, unsigned int> heard;       // the count at each stream's (by its id) last answer
 };
 
 namespace {
@@ -180,12 +185,21 @@ int moe_fp8_sync_status(moe_fp8_ctx_t *c, void *stream) {
     if (!c) return MOE_ERR_ARG;
     DeviceGuard g(c->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned int err = 0;
-    if (!g.ok || cudaMemcpyAsync(&err, c->err, sizeof err, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+    unsigned int count = 0;
+    unsigned long long id = 0;                  // (never used again, as a handle may be)
+    if (!g.ok || cudaStreamGetId(s, &id) != cudaSuccess ||
+        cudaMemcpyAsync(&count, c->err, sizeof count, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return MOE_ERR_CUDA;
-    if (!err) return MOE_OK;
-    if (cudaMemsetAsync(c->err, 0, 64, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!count) return MOE_OK;
+    try {
+        const std::lock_guard<std::mutex> hold(c->lock);
+        unsigned int &heard = c->heard[id];
+        if ((int)(count - heard) <= 0) return MOE_OK;
+        heard = count;
+    } catch (...) {
+        return MOE_ERR_NOMEM;
+    }
     return MOE_ERR_TIMEOUT;
 }
 
@@ -199,7 +213,7 @@ int moe_fp8_selftest_wait_timeout(moe_fp8_ctx_t *c, void *stream) {
     if (!c) return MOE_ERR_ARG;
     DeviceGuard g(c->device);
     if (!g.ok) return MOE_ERR_CUDA;
-    return status(launch_selftest_wait(c->err, c->wait_limit_ns, static_cast<cudaStream_t>(stream)));
+    return status(launch_fp8_selftest_wait(c->err, c->wait_limit_ns, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *c, int T, int d, int type, const void *x, int64_t ldx, const void *residual,

@@ -37,7 +37,7 @@
 // Tiles are walked rows fastest, so the B tile of neighbouring CTAs is the same and A stays in L2.
 //
 // Every wait is bounded (WaitCtl); when one runs out the CTA stops issuing, waits (bounded) for
-// what it has in flight, frees TMEM and returns with the error latched.
+// what it has in flight, frees TMEM and returns with the timeout counted.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -51,7 +51,7 @@ namespace moe {
 
 namespace {
 
-constexpr unsigned int FP8_ERR_WAIT = 1u;
+constexpr unsigned int FP8_ERR_WAIT = 1u;      // what a wait that runs out adds to the context's count
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
@@ -696,6 +696,25 @@ __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_c
     if (warp == MMA_WARP) tmem_dealloc_g<CTAS>(tmem, COLS);
 }
 
+// A wait on a barrier that nothing arrives at: it runs out, is counted, and the kernel ends.
+__global__ void fp8_selftest_wait_kernel(unsigned int *err, unsigned long long limit_ns) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const WaitCtl wc{&abort_flag, err, FP8_ERR_WAIT, limit_ns};
+    wait_phase_through(smem_addr(&bar), 0, wc);
+}
+
+cudaError_t launch_fp8_selftest_wait(unsigned int *err, unsigned long long limit_ns, cudaStream_t s) {
+    fp8_selftest_wait_kernel<<<1, 32, 0, s>>>(err, limit_ns);
+    return cudaGetLastError();
+}
+
 template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 static cudaError_t launch_t(const Fp8GemmParams &p, const Fp8Plan &pl, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -734,6 +753,8 @@ cudaError_t fp8_gemm_setup(int *clusters) {
     if (e == cudaSuccess) e = setup_t<256, 2, false, false, false>();
     if (e == cudaSuccess) e = setup_t<256, 2, false, false, true>();
     if (e == cudaSuccess) e = setup_t<256, 2, true, false, false>();
+    cudaFuncAttributes selftest;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&selftest, fp8_selftest_wait_kernel);
     for (int n = 1; n <= FP8_SPLIT_MAX && e == cudaSuccess; ++n) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n);

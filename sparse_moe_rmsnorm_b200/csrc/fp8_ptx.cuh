@@ -84,7 +84,7 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
             if (*w.abort) return false;
             if (now - start > (w.limit_ns >> 10)) {
                 *w.abort = 1;
-                atomicOr(w.err, w.err_bit);
+                atomicAdd(w.err, w.err_bit);        // (a count here: every stream hears of it)
                 return false;
             }
         }

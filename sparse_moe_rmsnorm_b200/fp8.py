@@ -189,7 +189,9 @@ class Fp8Ops:
         return self._c.gated_matmul(self.ctx, self._index, a, a_scale, w13, w13_scale, bias, alpha, limit, shift)
 
     def sync_status(self, stream=None) -> int:
-        """Waits for ``stream`` and returns MOE_OK, or MOE_ERR_TIMEOUT (once) where a device-side wait ran out."""
+        """Waits for ``stream`` and returns MOE_OK, or MOE_ERR_TIMEOUT where a device-side wait of any call of this
+        object ran out since this stream last asked: each stream hears of it once.  Streams that have to know whose
+        it was take an ``Fp8Ops`` each."""
         import torch
         return moe_fp8_sync_status(self.ctx, torch.cuda.current_stream(self._index) if stream is None else stream)
 

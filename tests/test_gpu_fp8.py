@@ -423,6 +423,29 @@ def test_wait_that_runs_out(ops):
     ops2.close()
 
 
+def test_every_stream_hears_of_a_wait_that_ran_out():
+    """Whichever asks first: the answer to one stream leaves another's alone; so does one between two timeouts."""
+    ops2 = moe.Fp8Ops()
+    moe.moe_fp8_set_wait_limit_ns(ops2.ctx, 2_000_000)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    assert ops2.sync_status(a) == ops2.sync_status(b) == moe.MOE_OK
+    moe.moe_fp8_selftest_wait_timeout(ops2.ctx, stream=b)
+    b.synchronize()
+    assert ops2.sync_status(a) == moe.MOE_ERR_TIMEOUT
+    assert ops2.sync_status(b) == moe.MOE_ERR_TIMEOUT
+    assert ops2.sync_status(a) == ops2.sync_status(b) == moe.MOE_OK
+    for s in (a, b):
+        moe.moe_fp8_selftest_wait_timeout(ops2.ctx, stream=s)
+    assert [ops2.sync_status(s) for s in (b, a, b, a)][:2] == [moe.MOE_ERR_TIMEOUT] * 2
+    torch.cuda.synchronize()
+    for s in (a, b):
+        ops2.sync_status(s)
+    assert ops2.sync_status(a) == ops2.sync_status(b) == moe.MOE_OK
+    assert ops2.sync_status() == moe.MOE_ERR_TIMEOUT            # the default stream's first question
+    assert ops2.sync_status() == moe.MOE_OK
+    ops2.close()
+
+
 def test_waits_do_not_count_the_kernel_before():
     """A product of few tiles and a very long K lasts longer than the limit of a single wait; the next product, which
     has SMs to start on meanwhile, waits for it without running out."""
