@@ -161,7 +161,8 @@ int moe_fp8_init(moe_fp8_ctx_t **out) {
         delete c;
         return MOE_ERR_NOMEM;
     }
-    if (cudaMemset(c->err, 0, 64) != cudaSuccess) {
+    // (waited for: streams that do not block on the default one are not behind it)
+    if (cudaMemset(c->err, 0, 64) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
         cudaFree(c->err);
         delete c;
         return MOE_ERR_CUDA;

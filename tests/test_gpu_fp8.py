@@ -423,6 +423,20 @@ def test_wait_that_runs_out(ops):
     ops2.close()
 
 
+def test_new_objects_start_clean_on_any_stream():
+    """The count is zero for a stream that is not ordered behind the default one, which is kept busy here."""
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        torch.cuda._sleep(2_000_000)
+        ops2 = moe.Fp8Ops()
+        moe.moe_fp8_set_wait_limit_ns(ops2.ctx, 1_000_000)
+        with torch.cuda.stream(s):
+            assert ops2.sync_status() == moe.MOE_OK
+        moe.moe_fp8_selftest_wait_timeout(ops2.ctx, stream=s)      # (its memory is not zero for the next one)
+        assert ops2.sync_status(s) == moe.MOE_ERR_TIMEOUT
+        ops2.close()
+
+
 def test_every_stream_hears_of_a_wait_that_ran_out():
     """Whichever asks first: the answer to one stream leaves another's alone; so does one between two timeouts."""
     ops2 = moe.Fp8Ops()
