@@ -79,6 +79,39 @@ def test_norm_of_a_row_added_to_itself(ops):
         assert torch.equal(a.float(), b.float())
 
 
+def test_one_row_in_place_under_another_stride(ops):
+    """One row's distance to the next means nothing: the same row is the same place whatever view it is."""
+    d, K = 272, 144
+    w = (1 + 0.3 * randn(d, seed=5)).to(BF16)
+    a, sa = rows(1, K, 1)
+    b, sb = weight(d, K, 2)
+    base, x = randn(4, 400, seed=1, dtype=BF16), randn(1, d, seed=2, dtype=BF16)
+    want = ops.add_rmsnorm(x, w, residual=base[1:2, :d].clone())
+    want_c = ops.matmul(a, sa, b, sb, residual=base[1:2, :d].clone())
+    for out_of in (lambda t: t[1, :d][None], lambda t: t[1:2, :d]):
+        for r_of in (lambda t: t[1, :d][None], lambda t: t[1:2, :d]):
+            buf = base.clone()
+            got = ops.add_rmsnorm(x, w, residual=r_of(buf), sum_out=out_of(buf))
+            for p, q in zip(got, want):
+                assert torch.equal(p.float(), q.float())
+            assert torch.equal(buf[1, :d], want[2][0])
+            buf[1, :d] = base[1, :d]
+            assert torch.equal(buf, base)
+            ops.matmul(a, sa, b, sb, residual=r_of(buf), out=out_of(buf))
+            assert torch.equal(buf[1, :d], want_c[0])
+            buf[1, :d] = base[1, :d]
+            assert torch.equal(buf, base)
+    # a column of results: its elements lie apart by the rows' distance alone
+    col = torch.zeros(6, 4, dtype=BF16, device="cuda")
+    a, sa = rows(6, K, 1)
+    b, sb = weight(1, K, 2)
+    want_c = ops.matmul(a, sa, b, sb, residual=col[:, 1:2].clone())
+    ops.matmul(a, sa, b, sb, residual=col[:, 1:2], out=col.t()[1:2].t())
+    assert torch.equal(col[:, 1:2], want_c) and (col[:, [0, 2, 3]] == 0).all()
+    with pytest.raises(moe.MoEError):                              # over its neighbour's first half
+        ops.matmul(a, sa, b, sb, residual=col[:, 1:2], out=col.view(-1)[:6].view(6, 1))
+
+
 def test_norm_zeros_infinities_and_nan(ops):
     """A row of zeros, and blocks of zeros, have the smallest scale and zero codes; a NaN spoils its own row
     only, an infinity makes its own block NaN and the rest of its row zero."""
