@@ -200,9 +200,9 @@ def _quantize(x, rows: int):
     import torch
     M, K = x.shape
     b = torch.nn.functional.pad(x.float(), (0, -K % FP8_BLOCK, 0, -M % rows))
-    b = b.view(b.shape[0] // rows, rows, -1, FP8_BLOCK)
+    b = b.view(b.shape[0] // rows, rows, b.shape[1] // FP8_BLOCK, FP8_BLOCK)
     s = (b.abs().amax(dim=(1, 3)) / FP8_MAX).clamp_min(FP8_SCALE_MIN)
-    q = (b / s[:, None, :, None]).reshape(b.shape[0] * rows, -1)[:M, :K]
+    q = (b / s[:, None, :, None]).reshape(b.shape[0] * rows, b.shape[2] * FP8_BLOCK)[:M, :K]
     return q.to(torch.float8_e4m3fn).contiguous(), s.contiguous()
 
 

@@ -143,6 +143,15 @@ def test_quantisers(M, K):
                 assert ((v - b).abs() <= b.abs() * (2.0 ** -4 + 2.0 ** -22) + s[i, j].double() * 2.0 ** -10).all()
 
 
+@pytest.mark.parametrize("M,K", [(0, 272), (0, 128), (3, 0), (0, 0)])
+def test_quantisers_of_nothing(M, K):
+    """An empty batch's rows and scales, as the operators take and give them."""
+    for quantise, rows in ((moe.quantize_fp8_rows, 1), (moe.quantize_fp8_weight, 128)):
+        q, s = quantise(torch.empty(M, K, dtype=torch.bfloat16))
+        assert q.shape == (M, K) and q.dtype == torch.float8_e4m3fn
+        assert s.shape == (-(-M // rows), -(-K // 128)) and s.dtype == torch.float32
+
+
 def test_stream_of_another_device_is_refused():
     """Its calls would run on the operators' device's current stream instead."""
     import types
