@@ -1,5 +1,6 @@
 """Build the sm_100a CUDA library ``libmoe_b200.so`` in-tree with nvcc, and ``_binding`` (its dense
-operators on torch tensors) with g++.
+operators on torch tensors) with g++ and torch's headers.  Where those are missing the library is built all the
+same, with a warning: everything but the dense operators works without ``_binding``.
 
     python -m sparse_moe_rmsnorm_b200.build [--force] [--verbose]
 
@@ -11,10 +12,12 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
 import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -45,10 +48,21 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _binding_stale(built_for: str) -> bool:
+    """Whether ``_binding`` is missing, older than its sources, or built for another torch than installed."""
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    if any(os.path.getmtime(p) > t for p in (BINDING_SRC, HEADER, __file__)):
+        return True
+    with open(BINDING, "rb") as f:
+        return built_for.encode() + b"\0" not in f.read()
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """The torch extension over the library (which it links, and has to be there)."""
-    deps = [BINDING_SRC, HEADER, __file__]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+    """The torch extension over the library (which it links, and has to be there).  Raises where it cannot be built."""
+    built_for = "moe_b200 binding for torch " + importlib.metadata.version("torch")
+    if not force and not _binding_stale(built_for):
         return BINDING
     import torch
     from torch.utils import cpp_extension
@@ -58,6 +72,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
                 *cpp_extension.include_paths(device_type="cuda")]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DMOE_BINDING_BUILT_FOR="%s"' % built_for,
            *[f for d in includes for f in ("-isystem", d)], "-o", tmp, BINDING_SRC,
            "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN",
            *["-L" + d for d in cpp_extension.library_paths(device_type="cuda")],
@@ -79,7 +94,11 @@ def build(force: bool = False, verbose: bool = False, nvcc: str = "nvcc") -> str
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    build_binding(force, verbose)
+    try:
+        build_binding(force, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:     # (no torch, no g++, no headers)
+        warnings.warn("libmoe_b200.so is built, but not the torch binding of the dense 8-bit operators, which needs "
+                      "torch with its headers and g++: %s: %s" % (type(e).__name__, e))
     return LIB
 
 

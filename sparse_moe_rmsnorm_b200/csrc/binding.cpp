@@ -188,6 +188,7 @@ py::tuple gated_matmul(uintptr_t ctx, int device, const Tensor &a, const Tensor 
 }  // namespace
 
 PYBIND11_MODULE(_binding, m) {
+    m.attr("built_for") = MOE_BINDING_BUILT_FOR;        // (the build looks for it in the file)
     m.def("set_error", [](py::object cls) { g_error = cls.release(); });
     m.def("add_rmsnorm", &add_rmsnorm);
     m.def("matmul", &matmul);

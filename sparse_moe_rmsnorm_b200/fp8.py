@@ -104,7 +104,8 @@ def _binding():
         try:
             mod = importlib.import_module("sparse_moe_rmsnorm_b200._binding")
         except ImportError as e:
-            raise RuntimeError("the torch binding is not built; run `python -m sparse_moe_rmsnorm_b200.build`") from e
+            raise RuntimeError("the torch binding is not built for this torch; run `python -m sparse_moe_rmsnorm_b200.build` "
+                               "(%s)" % e) from e
         mod.set_error(_moe.MoEError)
         _binding_module = mod
     return _binding_module

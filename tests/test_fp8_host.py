@@ -2,6 +2,9 @@
 quantisers against their definition."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -141,6 +144,44 @@ def test_quantisers(M, K):
                 v = q[i * rows:(i + 1) * rows, 128 * j:128 * (j + 1)].double() * s[i, j].double()
                 assert abs(s[i, j].double() - max(b.abs().max() / 448, 2.0 ** -126)) <= 2.0 ** -23 * s[i, j].double()
                 assert ((v - b).abs() <= b.abs() * (2.0 ** -4 + 2.0 ** -22) + s[i, j].double() * 2.0 ** -10).all()
+
+
+def test_build_goes_on_without_the_binding(lib, monkeypatch, tmp_path):
+    """Where the binding cannot be built the library is there all the same, and the operators that need the binding
+    say why they are not."""
+    for e in (FileNotFoundError("g++"), ModuleNotFoundError("No module named 'torch'"), subprocess.CalledProcessError(1, "g++")):
+        def fails(*_, e=e, **__):
+            raise e
+        monkeypatch.setattr(moe_build, "build_binding", fails)
+        with pytest.warns(UserWarning, match="torch binding"):
+            assert moe_build.build() == moe_build.LIB
+    monkeypatch.undo()
+    from sparse_moe_rmsnorm_b200 import fp8
+    monkeypatch.setattr(fp8, "_binding_module", None)
+    monkeypatch.setitem(sys.modules, "sparse_moe_rmsnorm_b200._binding", None)
+    with pytest.raises(RuntimeError, match="build.*None in sys.modules"):
+        fp8._binding()
+
+
+def test_binding_of_another_torch_is_built_again(lib, monkeypatch, tmp_path):
+    """A binding is kept only for the torch that it was built for, whatever the files' times are."""
+    import importlib.metadata
+    before = os.stat(moe_build.BINDING).st_mtime_ns
+    assert moe_build.build_binding() == moe_build.BINDING and os.stat(moe_build.BINDING).st_mtime_ns == before
+    copy = tmp_path / "_binding.so"
+    built = open(moe_build.BINDING, "rb").read()
+    copy.write_bytes(built)
+    monkeypatch.setattr(moe_build, "BINDING", str(copy))
+    ran = []
+    monkeypatch.setattr(moe_build.subprocess, "run", lambda cmd, **_: (ran.append(cmd), open(cmd[cmd.index("-o") + 1], "wb").close()))
+    moe_build.build_binding()
+    assert not ran
+    have = importlib.metadata.version("torch")
+    for other in ("0.0.1", have + "0", have[:-1]):
+        monkeypatch.setattr(moe_build.importlib.metadata, "version", lambda name, other=other: other)
+        moe_build.build_binding()
+        assert len(ran) == 1 and any(other in word for word in ran.pop())
+        copy.write_bytes(built)
 
 
 @pytest.mark.parametrize("M,K", [(0, 272), (0, 128), (3, 0), (0, 0)])
