@@ -68,7 +68,8 @@ extern "C" {
 #define MOE_ERR_ARG         -1   /* null pointer, bad size, misalignment, T > T_max, bad top_k */
 #define MOE_ERR_CUDA        -2   /* a CUDA runtime call or kernel launch failed */
 #define MOE_ERR_TIMEOUT     -3   /* a device-side bounded wait ran out (latched) */
-#define MOE_ERR_UNSUPPORTED -4   /* not a compute capability 10.0 device */
+#define MOE_ERR_UNSUPPORTED -4   /* not a compute capability 10.0 device (moe_fp8_init: or built by a
+                                    compiler that gave the products' kernels other registers than they share out) */
 #define MOE_ERR_NOMEM       -5   /* device workspace allocation failed */
 
 typedef struct {

@@ -278,7 +278,7 @@ const char *moe_strerror(int code) {
         case MOE_ERR_ARG: return "invalid argument";
         case MOE_ERR_CUDA: return "CUDA error";
         case MOE_ERR_TIMEOUT: return "device-side wait timed out";
-        case MOE_ERR_UNSUPPORTED: return "unsupported device (needs compute capability 10.0)";
+        case MOE_ERR_UNSUPPORTED: return "unsupported device (needs compute capability 10.0) or build of the library";
         case MOE_ERR_NOMEM: return "out of device memory";
         default: return "unknown error";
     }

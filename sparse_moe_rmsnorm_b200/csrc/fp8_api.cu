@@ -152,9 +152,12 @@ int moe_fp8_init(moe_fp8_ctx_t **out) {
     c->wait_limit_ns = 2000000000ull;
     memset(c->clusters, 0, sizeof c->clusters);
     // (every kernel is loaded here, so that a first call may be captured)
-    if (fp8_gemm_setup(c->clusters) != cudaSuccess || fp8_few_setup() != cudaSuccess || fp8_norm_setup() != cudaSuccess) {
+    cudaError_t e = fp8_gemm_setup(c->clusters);
+    if (e == cudaSuccess) e = fp8_few_setup();
+    if (e == cudaSuccess) e = fp8_norm_setup();
+    if (e != cudaSuccess) {
         delete c;
-        return MOE_ERR_CUDA;
+        return e == cudaErrorNotSupported ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
     }
     if (cudaMalloc(&c->err, 64) != cudaSuccess) {
         cudaGetLastError();

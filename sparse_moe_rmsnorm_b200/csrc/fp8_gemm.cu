@@ -735,10 +735,11 @@ static cudaError_t launch_t(const Fp8GemmParams &p, const Fp8Plan &pl, cudaStrea
 
 template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 static cudaError_t setup_t() {
-    // the registers that the kernel's warpgroups share out have to be there at launch
+    // the registers that the kernel's warpgroups share out have to be there at launch (setmaxnreg waits for them), and
+    // another compiler may give the kernel fewer
     cudaFuncAttributes attr;
     cudaError_t e = cudaFuncGetAttributes(&attr, fp8_gemm_kernel<BN, CTAS, GATED, SK, RES>);
-    if (e == cudaSuccess && attr.numRegs != 168) e = cudaErrorInvalidKernelImage;
+    if (e == cudaSuccess && attr.numRegs != 168) e = cudaErrorNotSupported;
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(fp8_gemm_kernel<BN, CTAS, GATED, SK, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, FP8_SMEM_SM);
 }
