@@ -615,3 +615,153 @@ def test_refusals(ops):
             pytest.fail("case %d was accepted" % i)
         assert e.value.code == moe.MOE_ERR_ARG
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------- the hard cases, in every form
+
+# few rows, single tiles, K split over a cluster, CTA pairs; gated: few rows, a split tile, one CTA's, CTA pairs
+FORMS = {"few": (9, 300, 400), "single": (70, 19101, 144), "split": (140, 300, 400), "pair": (600, 5000, 272)}
+GATED_FORMS = {"few": (9, 272, 256), "split": (40, 272, 256), "single": (100, 19104, 128), "pair": (600, 2496, 272)}
+
+
+def as_planned(form, gated):
+    M, N, K = (GATED_FORMS if gated else FORMS)[form]
+    pl = moe.moe_fp8_debug_plan(gated, M, N, K, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert form == ("few" if pl["few"] else "pair" if pl["ctas"] == 2 else "split" if pl["split"] > 1 else "single")
+    return M, N, K
+
+
+def gated_weight(F, K, seed):
+    gate, linear = weight(F, K, seed), weight(F, K, seed + 1)
+    return torch.cat([gate[0].view(torch.uint8), linear[0].view(torch.uint8)]), torch.stack([gate[1], linear[1]])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_nan_and_infinity_in_every_form(ops, form, with_residual):
+    """A NaN code or an infinite scale of a row spoils its row, of a weight its column (its 128 columns); a row of zeros
+    gives zeros (or the residual); everything else comes out with the same bits."""
+    M, N, K = as_planned(form, False)
+    a, sa = rows(M, K, 1)
+    b, sb = weight(N, K, 2)
+    res = randn(M, N, seed=3, dtype=BF16) if with_residual else None
+    zero, nan, inf, col, block = M // 2, 1, M - 2, 17, (N - 1) // 128
+    a.view(torch.uint8)[zero] = 0
+    want = ops.matmul(a, sa, b, sb, residual=res)
+    assert torch.equal(want[zero], res[zero] if with_residual else torch.zeros_like(want[zero]))
+    a2, sa2, b2, sb2 = a.clone(), sa.clone(), b.clone(), sb.clone()
+    a2.view(torch.uint8)[nan, K - 1] = 0x7F
+    sa2[inf, -1] = math.inf
+    b2.view(torch.uint8)[col, 5] = 0xFF
+    sb2[block, 0] = math.nan
+    c = ops.matmul(a2, sa2, b2, sb2, residual=res)
+    keep = torch.ones(M, N, dtype=torch.bool, device="cuda")
+    keep[nan] = keep[inf] = False
+    keep[:, col] = False
+    keep[:, 128 * block:] = False
+    assert c[nan].isnan().all() and not torch.isfinite(c[inf]).any()
+    assert c[:, col].isnan().all() and c[:, 128 * block:].isnan().all()
+    assert torch.equal(c[keep], want[keep])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_far_scales_in_every_form(ops, form):
+    """Scales that are no powers of two, across the fp32 range, and zero ones."""
+    M, N, K = as_planned(form, False)
+    a, sa = rows(M, K, 3)
+    b, sb = weight(N, K, 4)
+    kb = torch.arange(sa.shape[1], device="cuda")
+    sa = sa * torch.tensor([1e-18, 3e-7, 1.0, 1e12], device="cuda")[kb] * torch.tensor([1.0, 1e-3, 0.0, 7.7], device="cuda")[torch.arange(M, device="cuda") % 4, None]
+    sb = sb * torch.tensor([1e15, 1e6, 1.7, 1e-12], device="cuda")[kb]
+    c = ops.matmul(a, sa, b, sb, out_dtype=FP32)
+    want, tol = product_ref(a, sa, b, sb)
+    # (and a step of the smallest numbers for each product of codes)
+    assert ((c.double() - want).abs() <= tol + (want.abs() + tol) * half_step(FP32) + K * 448 ** 2 * 2.0 ** -149).all()
+    assert (c[2::4] == 0).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("place", ["odd", "even", "16 bytes"])
+def test_strides_in_every_form(ops, form, dtype, place):
+    """Rows of a, of the residual and of the result apart and anywhere: the same bits, and nothing around the result
+    or between its rows is touched; in place of the residual too."""
+    M, N, K = as_planned(form, False)
+    a, sa = rows(M, K, 1)
+    b, sb = weight(N, K, 2)
+    bias, res = randn(N, seed=3, dtype=BF16), randn(M, N, seed=7, dtype=dtype)
+    want = ops.matmul(a, sa, b, sb, bias=bias, residual=res)
+    abuf = torch.full((M + 1, K + 48), 0x7F, dtype=torch.uint8, device="cuda")      # NaN between the rows
+    abuf[1:, 16:16 + K] = a.view(torch.uint8)
+    at, pad, rpad = {"odd": (3, 5, 2), "even": (2, 2 + N % 2, 4 + N % 2), "16 bytes": (16, 16 - N % 8, 24 - N % 8)}[place]
+    base = torch.full((at + M * (N + pad) + 9,), 7.0, dtype=dtype, device="cuda")
+    c = base[at:at + M * (N + pad)].view(M, N + pad)[:, :N]
+    rbuf = torch.zeros(M, N + rpad, dtype=dtype, device="cuda")
+    rbuf[:, :N] = res
+    for r in (rbuf[:, :N], c):
+        if r is c:
+            c.copy_(res)
+        got = ops.matmul(abuf[1:, 16:16 + K], sa, b, sb, bias=bias, residual=r, out=c)
+        assert got.data_ptr() == c.data_ptr() and torch.equal(c, want)
+        c.fill_(7.0)
+        assert (base == 7).all()
+
+
+@pytest.mark.parametrize("form", GATED_FORMS)
+def test_gated_nan_and_zero_rows_in_every_form(ops, form):
+    """A NaN in a row makes that row's scales and codes NaN, a row of zeros (without a bias) the smallest scale and
+    zero codes; the other rows keep their bits.  Rows of a apart, NaN codes between them."""
+    M, F, K = as_planned(form, True)
+    a, sa = rows(M, K, 1)
+    w13, w13s = gated_weight(F, K, 2)
+    zero, nan = M // 2, M - 2
+    a.view(torch.uint8)[zero] = 0
+    want = ops.gated_matmul(a, sa, w13, w13s)
+    assert (want[1][zero] == SCALE_MIN).all() and (want[0][zero].float() == 0).all()
+    abuf = torch.full((M + 1, K + 48), 0x7F, dtype=torch.uint8, device="cuda")
+    abuf[1:, 16:16 + K] = a.view(torch.uint8)
+    got = ops.gated_matmul(abuf[1:, 16:16 + K], sa, w13, w13s)
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+    a.view(torch.uint8)[nan, K - 1] = 0x7F
+    h, s = ops.gated_matmul(a, sa, w13, w13s)
+    assert s[nan].isnan().all() and h[nan].float().isnan().all()
+    rest = [i for i in range(M) if i != nan]
+    assert torch.equal(h.view(torch.uint8)[rest], want[0].view(torch.uint8)[rest]) and torch.equal(s[rest], want[1][rest])
+
+
+@pytest.mark.parametrize("form", GATED_FORMS)
+def test_gated_infinities_in_every_form(ops, form):
+    """The clamps take an infinite gate (+) and linear value (+ or -) as they take any large one; a gate of -inf is
+    -inf * 0: its block's scale and codes are NaN.  Without clamps an infinite value makes its block's scale infinite,
+    its own code NaN and the others zero.  Other blocks keep their bits."""
+    M, F, K = as_planned(form, True)
+    a, sa = rows(M, K, 5)
+    w13, w13s = gated_weight(F, K, 6)
+    bias = randn(2 * F, seed=8, dtype=BF16)
+    last = F - 1
+    big, inf = bias.clone(), bias.clone()
+    for col, v in ((3, 1e4), (F + 5, 1e4), (F + last, -1e4), (F + 64, 1e4)):
+        big[col], inf[col] = v, math.copysign(math.inf, v)
+    want, got = ops.gated_matmul(a, sa, w13, w13s, bias=big), ops.gated_matmul(a, sa, w13, w13s, bias=inf)
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+    y, tol = gated_ref(a, sa, w13, w13s, big, *ACTS["clamped"])
+    check_codes(want[0], want[1], y, tol)
+
+    inf[130] = -math.inf
+    h, s = ops.gated_matmul(a, sa, w13, w13s, bias=inf)
+    other = torch.ones(F, dtype=torch.bool, device="cuda")
+    other[128:256] = False
+    assert s[:, 1].isnan().all() and h.float()[:, ~other].isnan().all()
+    assert torch.equal(h.view(torch.uint8)[:, other], want[0].view(torch.uint8)[:, other])
+    assert torch.equal(torch.cat([s[:, :1], s[:, 2:]], 1), torch.cat([want[1][:, :1], want[1][:, 2:]], 1))
+
+    silu = dict(alpha=1.0, limit=math.inf, shift=0.0)
+    want = ops.gated_matmul(a, sa, w13, w13s, bias=bias, **silu)
+    bias2 = bias.clone()
+    bias2[130] = math.inf
+    h, s = ops.gated_matmul(a, sa, w13, w13s, bias=bias2, **silu)
+    assert (s[:, 1] == math.inf).all() and h[:, 130].float().isnan().all()
+    rest = ~other
+    rest[130] = False
+    assert (h.float()[:, rest] == 0).all()
+    assert torch.equal(h.view(torch.uint8)[:, other], want[0].view(torch.uint8)[:, other])
