@@ -49,9 +49,10 @@ struct Fp8GemmParams {
 };
 
 // The same products for up to FP8_FEW rows (fp8_few.cu), as long as its CTAs are all there at once; beyond that the
-// persistent kernel is as good or better.  Here | there, us: 1 x 5120 x 2880 4.6 | 11, 16 x 5120 x 2880 8.9 | 9.2,
-// 16 x 40000 x 2880 31.0 | 29.7, 8 x 40000 x 528 13.8 | 10.6, 8 x 201088 x 2880 127 | 122 (though 1 x 40000 x 2880
-// 25.2 | 29.5); gated 16 x 2880 x 2880 9.0 | 9.5, 16 x 11520 x 2880 24.6 | 21.4.
+// persistent kernel is as good or better, but for one to four rows and a long K, where it is up to a sixth behind.  Here |
+// there, us: 1 x 5120 x 2880 4.6 | 11, 16 x 5120 x 2880 8.9 | 9.2, 16 x 40000 x 2880 31.0 | 29.7, 8 x 40000 x 528 13.8 |
+// 10.6, 1 x 40000 x 528 13.2 | 10.3, 8 x 201088 x 2880 127 | 122, but 1 x 40000 x 2880 25.2 | 29.5, 4 x 100000 x 2880
+// 60.9 | 65.6; gated 16 x 2880 x 2880 9.0 | 9.5, 16 x 11520 x 2880 24.6 | 21.4, but 1 x 20000 x 2880 36.3 | 39.2.
 constexpr int FP8_FEW = 16;
 constexpr int FP8_FEW_CTAS = 3;         // CTAs (16 columns each) to an SM, at most
 inline bool fp8_few(int M, int N, int gated, int num_sms) {
@@ -144,18 +145,21 @@ inline bool fp8_plan(int M, int N, int K, int gated, int num_sms, const int *clu
     if (M > FP8_SIZE_MAX || N > FP8_SIZE_MAX || K > FP8_SIZE_MAX) return false;
     long long rows = (M + FP8_BM - 1) / FP8_BM;
     const long long cols = fp8_blocks(N), wide = gated ? cols : (N + 255) / 256;     // columns in 128s, in pairs' tiles
-    // The form that should take least: us per K block (of hand-overs, mostly) and per tile, as measured.  Either side
-    // of its choices, us: 1024 x 5120 x 2880 single 27.9, pairs 30.9; 1500 x 5120 x 2880 39.7, 34.9; 8192 x 5120 x 2880
-    // 180, 155; 130 x 5120 x 2880 split 10.6, pairs 16.6; 24 x 5120 x 11520 split 16.3, single 29.3; gated 512 x 2880 x
-    // 2880 split 26.5, pairs 17.7, 64 x 2880 x 2880 split 10.4, not split 20.9.
+    // The form that should take least: us per K block (of hand-overs, mostly) and per tile, as fitted to measured times
+    // (the gated forms' within a seventh).  Either side of its choices, us: 1024 x 5120 x 2880 single 27.3, pairs
+    // 30.4; 1500 x 5120 x 2880 37.1, 32.8; 8192 x 5120 x 2880 180, 155; 256 x 2880 x 6144 split 13.6, pairs 27.2;
+    // 24 x 5120 x 11520 split 16.3, single 29.3.  Gated, split | pairs (weights from memory): 256 x 2880 x 512 10.7 |
+    // 6.8, 333 x 1360 x 1552 12.3 | 11.2, 256 x 2880 x 2880 17.8 | 16.4, 512 x 2880 x 2880 26.7 | 17.4, 260 x 1360 x
+    // 2880 14.0 | 15.9, 256 x 2880 x 6144 25.8 | 28.0; 64 x 2880 x 2880 split 10.4, not split 20.9.
     const int kb = fp8_blocks(K);
     auto waves = [](long long tiles, int at_once) { return at_once > 0 ? (double)((tiles + at_once - 1) / at_once) : 1e30; };
     const long long pair_tiles = (rows + 1) / 2 * wide, one_tiles = rows * cols;
     int n = 1;                                  // CTAs to split K over
     while (n < FP8_SPLIT_MAX && n < kb && one_tiles <= clusters[n + 1]) ++n;
-    const double per_kb = gated ? 0.6 : 0.34, pair = waves(pair_tiles, num_sms / 2) * (0.55 * kb + 3.0);
-    const double one = n > 1 || gated ? waves(one_tiles, clusters[n]) * (per_kb * ((kb + n - 1) / n) + 4.0)
-                                      : waves(one_tiles, num_sms) * (per_kb * kb + 2.0);
+    const double pair = waves(pair_tiles, num_sms / 2) * (gated ? 0.48 * kb + 4.7 : 0.55 * kb + 3.0);
+    const double one = gated   ? waves(one_tiles, clusters[n]) * (0.7 * ((kb + n - 1) / n) + 9.5)
+                       : n > 1 ? waves(one_tiles, clusters[n]) * (0.34 * ((kb + n - 1) / n) + 4.0)
+                               : waves(one_tiles, num_sms) * (0.34 * kb + 2.0);
     pl->bn = gated ? 256 : 128;
     pl->ctas = 1;
     pl->split = n;

@@ -104,6 +104,14 @@ def test_plans_fit_and_cover(lib, gated, M):
             assert not pl["few"] or M <= 16
 
 
+def test_gated_form_that_measured_faster(lib):
+    """Pairs or K split, at the sizes whose times stand beside the rule."""
+    for form, sizes in (("pair", [(256, 2880, 512), (333, 1360, 1552), (512, 2880, 2880), (2000, 272, 1040)]),
+                        ("split", [(260, 1360, 2880), (256, 2880, 6144), (1200, 256, 2880), (64, 2880, 2880)])):
+        for s in sizes:
+            assert (moe.moe_fp8_debug_plan(True, *s, 148)["ctas"] == 2) == (form == "pair"), s
+
+
 def test_gpu_sizes_cover_every_form(lib):
     """The sizes of the GPU tests run every kernel: the one for a few rows, pairs, single tiles, split K (and, gated,
     a split tile with one CTA), each with ragged rows and columns."""

@@ -318,6 +318,15 @@ def test_gated(ops, M, F, K, act, with_bias):
     assert torch.equal(h.view(torch.uint8), h2.view(torch.uint8)) and torch.equal(hs, hs2)
 
 
+@pytest.mark.parametrize("M,F,K", [(129, 640, 6144), (200, 272, 2064), (333, 144, 2880), (1200, 256, 2880), (400, 1360, 4112)])
+@pytest.mark.parametrize("act", sorted(ACTS))
+def test_gated_split_over_many_row_tiles(ops, M, F, K, act):
+    """K split over a cluster where there are several tiles of rows, too: a long K and few columns."""
+    pl = moe.moe_fp8_debug_plan(True, M, F, K, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert pl["split"] > 1 and pl["m_tiles"] > 1 and not pl["few"]
+    test_gated(ops, M, F, K, act, True)
+
+
 def test_gated_zero_and_nan_rows(ops):
     M, F, K = 40, 272, 256
     a, sa = rows(M, K, 1)
