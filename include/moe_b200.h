@@ -263,8 +263,10 @@ MOE_API int moe_forward_noalloc(int T, int d_model, int d_ff, int n_experts, int
  *   weights      u8 [N, K] and fp32 [ceil(N/128), ceil(K/128)]: a scale for each
  *                128 x 128 block (blocks at the right and lower edges are smaller)
  * E4M3 outputs take the scale s = max(max|v| / 448, 2^-126) of their block and
- * round v / s to nearest even.  Products and sums are fp32; an output is rounded
- * once.  A NaN in a block makes its scale and all its codes NaN.
+ * round v * (1 / s), reciprocal and product in fp32, to nearest even (so next to a tie a
+ * code can be the neighbour of the one that v / s rounds to).  Products and sums are fp32;
+ * a 16- or 32-bit output is rounded once.  A NaN in a block makes its scale and all its codes
+ * NaN; an infinite |v| makes the scale infinite or NaN, its own code NaN and the others zero or NaN.
  *
  * No call allocates or keeps anything: there is no workspace, and calls on one
  * context may overlap (streams, host threads, captured graphs).  Results do not
@@ -298,6 +300,7 @@ MOE_API int moe_fp8_selftest_wait_timeout(moe_fp8_ctx_t *ctx, void *stream);
  * q, q_scale = n / sqrt(mean(n^2) + eps) * norm_scale in E4M3.
  * x, residual, sum_out: type [T, d], rows ldx / ldr / lds elements apart (whole
  * 16-byte units); norm_scale bf16 [d]; q u8 [T, d]; q_scale fp32 [T, ceil(d/128)].
+ * All but q_scale start on 16 bytes.
  * d: multiple of 16, 16..16384. */
 MOE_API int moe_add_rmsnorm_fp8(moe_fp8_ctx_t *ctx, int T, int d, int type, const void *x, int64_t ldx,
                         const void *residual, int64_t ldr, const uint16_t *norm_scale, float eps, void *sum_out,
@@ -317,8 +320,9 @@ MOE_API int moe_fp8_matmul(moe_fp8_ctx_t *ctx, int M, int N, int K, const uint8_
  *   h = g * sigmoid(alpha g) * (u + shift), then E4M3 with a scale per 128 columns.
  * (alpha, limit, shift) = (1.702, 7, 1) is the experts' activation, (1, INFINITY, 0) is
  * silu(gate) * linear; alpha and shift are finite, limit > 0.  a, a_scale as above;
- * w13 u8 [2, F, K] (gate rows, then linear rows), w13_scale fp32 [2, ceil(F/128), ceil(K/128)] (each half has its own blocks), b13 bf16
- * [2, F] or NULL; h u8 [M, F], h_scale fp32 [M, ceil(F/128)].  F a multiple of 16. */
+ * w13 u8 [2, F, K] (gate rows, then linear rows), w13_scale fp32 [2, ceil(F/128), ceil(K/128)]
+ * (each half has its own blocks), b13 bf16 [2, F] or NULL; h u8 [M, F], h_scale fp32
+ * [M, ceil(F/128)].  F a multiple of 16; w13 and h 16-byte aligned. */
 MOE_API int moe_fp8_gated_matmul(moe_fp8_ctx_t *ctx, int M, int F, int K, const uint8_t *a, int64_t lda,
                          const float *a_scale, const uint8_t *w13, const float *w13_scale, const uint16_t *b13,
                          float alpha, float limit, float shift, uint8_t *h, float *h_scale, void *stream);

@@ -9,9 +9,10 @@
 // form of mma.sync), scales each K block's sums in registers, and the CTA's eight warps, which split
 // K, add up at the end in a fixed order.
 //
-// One token, in a run of calls: 5120 x 2880 in 4.6 us (14.8 MB, 3.2 TB/s; 10.2 in the other kernel), gated
-// 2 x 2880 x 2880 in 6.2 us (16.6 MB, 2.7 TB/s; 11.8): latency, of the launch, of one round of loads (eight
-// of ten samples of a warp wait for memory) and of the join, and for the gated form of the cluster's exchange.
+// One token, in a run of calls on weights that L2 holds in part: 5120 x 2880 in 4.6 us (10.2 in the other kernel),
+// gated 2 x 2880 x 2880 in 6.3 us (11.8); all weights from memory: 5.7 us (14.8 MB, 2.6 TB/s) and 7.5 us (16.6 MB,
+// 2.2 TB/s).  Latency: of the launch, behind which the loads start, of one round of loads (eight of ten samples of a
+// warp wait for memory) and of the join, and for the gated form of the cluster's exchange.
 //
 // Operands without shuffles: the K order within a product is free as long as both sides use the
 // same.  Lane (g, t) takes the 16 bytes t of a 64-byte K segment of rows g and g + 8 (of token g); each of their

@@ -7,9 +7,12 @@
 // own in TMEM.  The scales are any fp32 numbers, so the tensor core cannot apply them: the
 // epilogue warps read each block's accumulator, multiply by sa * sb (one number per thread and
 // 64 or 128 columns: a thread holds one row) and add it to fp32 sums in registers, while the
-// MMAs fill the next accumulator.  That is one FMA and one word of TMEM per 128 products, and it, not the MMA,
-// bounds large products: the MMAs and copies of 8192 x 5120 x 2880 alone take 88 us (at the power limit's clock),
-// with the sums 145 to 158 us, 1.5 to 1.7 PFLOP/s, the tensor pipe 45% and the issue slots 51% busy.
+// MMAs fill the next accumulator.  That is one FMA and one word of TMEM per 128 products.  Large products: 8192 x
+// 5120 x 2880 takes 143 to 157 us, 1.5 to 1.7 PFLOP/s, the MMAs and copies alone 88 (at the power limit's clock).  A
+// 256-column K block takes 0.6 us, some 960 clocks, where the MMAs need 512 at their nominal rate and the sums 579
+// in isolation; the tensor pipe is 45% and the issue slots 51% busy, so neither is the bound by itself (whether they
+// contend for TMEM or the hand-overs show has not been told apart).  A tile's start and end, which no MMA covers, are
+// another 3 us, nine times here.
 //
 // Gated (both projections of a gated feed-forward block): a CTA's accumulator columns are half
 // gate rows and half linear rows of W13, so a thread holds a row's gate and linear value of the
@@ -23,13 +26,14 @@
 //           parts of 128 columns, one per epilogue warpgroup, each filled and freed by itself.  (Gated,
 //           8192 x 2 x 2880 x 2880: 163 to 171 us, 1.6 to 1.7 PFLOP/s.)
 //   single  128 x 128 tiles, one CTA each, persistent: few rows by many columns, or too few tiles for pairs.
-//           64 rows by 201088 columns (fp32 out), K = 2880: 118 to 133 us, 631 MB at 4.7 to 5.3 TB/s; a tile's
-//           23 K blocks at 0.34 us of hand-overs are what it waits for.  1024 x 5120 x 2880: 28 us.
+//           64 rows by 201088 columns (fp32 out), K = 2880: 132 us at 1965 MHz in a run of calls with a new result
+//           each (631 MB at 4.8 TB/s), 124 into the same two results; a tile's 23 K blocks at 0.34 us of hand-overs
+//           are what it waits for.  1024 x 5120 x 2880: 28 us.
 //   split   few tiles: the CTAs of a cluster split K (a block costs a CTA some 0.2 us of hand-overs whatever
 //           its size, so the chain of blocks is what takes the time), then join their sums through
 //           distributed shared memory, in a fixed order, each finishing some of the rows.  32 x 5120 x 2880:
-//           7.3 us in a run of calls (10.5 with K whole), 15 MB that HBM could bring in 2.3: 8 blocks' hand-overs,
-//           the join and the launch.
+//           7.3 us in a run of calls (10.5 with K whole) and 8.9 with all weights from memory, 15 MB that HBM could
+//           bring in 2.3: 8 blocks' hand-overs, the join and the launch.
 //
 // Warp roles: 8 epilogue warps (warp w reads TMEM lane quarter w % 4), the TMA producer, two MMA
 // warps, one elected lane of each running its loop, then the warp that fetches the scales (16 K
@@ -349,7 +353,7 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity, unsig
 }  // namespace
 
 // RES: with a residual (a kernel of its own, as its code made the others' slower: see store_columns).  2048 x 5120 x
-// 2880 bf16: 55 us with one, 46 without: the reads of it are eight rounds of loads a tile (fewer, of 32 steps, spill).
+// 2880 bf16: 57 us with one, 47 without: the reads of it are eight rounds of loads a tile (fewer, of 32 steps, spill).
 template <int BN, int CTAS, bool GATED, bool SK, bool RES>
 __global__ void __launch_bounds__(FP8_THREADS, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmParams p) {
     constexpr int WGS = FP8_WGS;                // epilogue warpgroups

@@ -1,14 +1,15 @@
 // RMS norm with the residual's addition, the normalised rows in E4M3 with a scale per 128 elements.
 //
 //   n = x + r,  y = n / sqrt(mean(n^2) + eps) * w          (fp32 throughout)
-//   s_b = max(max_{i in b} |y_i| / 448, 2^-126),  q = e4m3(y / s_b)
+//   s_b = max(max_{i in b} |y_i| / 448, 2^-126),  q = e4m3(y (1 / s_b))
 //
 // The norm is the routed block's (no bias, no mean subtraction: pnsm.cn overview, section 2.3;
 // "gpt-oss-20B" hub page, section 3.2) and stands beside it: here the rows leave in the form the
 // dense 8-bit products read.  Bound by HBM: x, r, the sum and q move once (8192 rows of 2880, bf16:
-// 166 MB in 28.8 us alone and 30.0 in a run of calls, 0.88 and 0.84 of the measured copy rate), and next by
-// instruction issue (75% of the slots): the arithmetic is on pairs (f32x2), which took it from 39 us.  One CTA holds a row in registers, 8 or 16 elements per
-// thread, so the row is read once and the second pass (the scaling) needs no memory; a block's 128
+// 166 MB in 30.2 us in a run of calls, 27.3 from a graph whose calls write the same results, 0.84 and 0.92 of the
+// measured copy rate), and next by instruction issue (75% of the slots): the arithmetic is on pairs (f32x2), which
+// took it from 39 us.  One row: 1.5 us from a graph, a launch; in a run of calls the host's 5.  One CTA holds a row in
+// registers, 8 or 16 elements per thread, so the row is read once and the second pass (the scaling) needs no memory; a block's 128
 // elements sit in 16 neighbouring lanes, so its maximum is four shuffles.  A row's sum adds the
 // elements of a thread in two halves, then a tree over lanes and warps.
 #include <cuda_bf16.h>

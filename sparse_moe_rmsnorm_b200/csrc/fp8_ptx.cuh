@@ -32,18 +32,13 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Arrive on a barrier of any CTA of the cluster (address from map_to_rank), releasing this
-// thread's earlier writes at cluster scope.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same without the cluster-scope release (which waits for all of the thread's memory operations):
-// for a barrier that orders tensor memory alone, after tcgen05.wait and its fence.
+// Arrive on a barrier of any CTA of the cluster (address from map_to_rank), without a cluster-scope release (which
+// waits for all of the thread's memory operations): for a barrier that orders tensor memory alone, after
+// tcgen05.wait and its fence.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }

@@ -8,6 +8,9 @@ of a row (``[M, ceil(K/128)]``), weights ``[N, K]`` one for each 128 x 128 block
 Like the rest of the package this only checks and marshals arguments (``Fp8Ops`` does so in C++,
 ``csrc/binding.cpp``): the work is in the CUDA library, every call raises where the library or a B200
 is missing, and a call returns when its kernel is queued.
+
+There is no backward pass: results carry no gradient, also where an operand asks for one, and a tracer that
+runs these calls would record their results as constants.
 """
 from __future__ import annotations
 
