@@ -319,7 +319,7 @@ MOE_API int moe_fp8_matmul(moe_fp8_ctx_t *ctx, int M, int N, int K, const uint8_
  *   g = min(W13_gate a + b_gate, limit),  u = clamp(W13_linear a + b_linear, -limit, limit),
  *   h = g * sigmoid(alpha g) * (u + shift), then E4M3 with a scale per 128 columns.
  * (alpha, limit, shift) = (1.702, 7, 1) is the experts' activation, (1, INFINITY, 0) is
- * silu(gate) * linear; alpha and shift are finite, limit > 0.  a, a_scale as above;
+ * silu(gate) * linear; |alpha| <= 2^127, shift is finite, limit > 0.  a, a_scale as above;
  * w13 u8 [2, F, K] (gate rows, then linear rows), w13_scale fp32 [2, ceil(F/128), ceil(K/128)]
  * (each half has its own blocks), b13 bf16 [2, F] or NULL; h u8 [M, F], h_scale fp32
  * [M, ceil(F/128)].  F a multiple of 16; w13 and h 16-byte aligned. */

@@ -289,14 +289,15 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
                          const uint8_t *w13, const float *w13_scale, const uint16_t *b13, float alpha, float limit,
                          float shift, uint8_t *h, float *h_scale, void *stream) {
     int rc = check_product(c, M, F, K, a, lda, a_scale, w13, w13_scale, b13);
-    if (rc || F % 16 || !(limit > 0.0f) || !std::isfinite(alpha) || !std::isfinite(shift)) return MOE_ERR_ARG;
+    const float minus_alpha_log2e = -1.44269504f * alpha;
+    if (rc || F % 16 || !(limit > 0.0f) || !std::isfinite(minus_alpha_log2e) || !std::isfinite(shift)) return MOE_ERR_ARG;
     if (M == 0) return MOE_OK;
     if (!aligned(h, 16) || !aligned(h_scale, 4)) return MOE_ERR_ARG;
     DeviceGuard g(c->device);
     if (!g.ok) return MOE_ERR_CUDA;
     if (fp8_few(M, F, 1, c->num_sms)) {
         Fp8FewParams p = few_params(M, F, K, a, lda, a_scale, w13, w13_scale, b13);
-        p.minus_alpha_log2e = -1.44269504f * alpha;
+        p.minus_alpha_log2e = minus_alpha_log2e;
         p.limit = limit;
         p.shift = shift;
         p.h = h;
@@ -306,7 +307,7 @@ int moe_fp8_gated_matmul(moe_fp8_ctx_t *c, int M, int F, int K, const uint8_t *a
     Fp8GemmParams p;
     Fp8Plan pl;
     if ((rc = product_params(c, p, pl, 1, M, F, K, a, lda, a_scale, w13, w13_scale, b13))) return rc;
-    p.minus_alpha_log2e = -1.44269504f * alpha;
+    p.minus_alpha_log2e = minus_alpha_log2e;
     p.limit = limit;
     p.shift = shift;
     p.h = h;

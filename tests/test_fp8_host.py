@@ -67,6 +67,15 @@ def test_sizes_types_strides_and_alignment(lib):
     assert lib.moe_fp8_gated_matmul(c, 0, 32, 64, None, 0, None, None, None, None, 1.0, 7.0, 1.0, None, None, None) == moe.MOE_OK
 
 
+def test_alpha_past_the_range_of_its_exponent_is_refused(lib):
+    """The exponent is alpha log2(e) g in fp32: where alpha log2(e) is no number, 0 times it would not be 0."""
+    c, P = ctypes.byref(Ctx(0, 148, None, 1)), 1 << 20
+    for alpha in (2.0 ** 127 * 1.5, -2.0 ** 127 * 1.5, 3.4e38):
+        assert lib.moe_fp8_gated_matmul(c, 4, 32, 64, P, 64, P, P, P, None, alpha, 7.0, 1.0, P, P, None) == moe.MOE_ERR_ARG
+    # (no rows: nothing else to check)
+    assert lib.moe_fp8_gated_matmul(c, 0, 32, 64, None, 64, None, None, None, None, 2.0 ** 127, 7.0, 1.0, None, None, None) == moe.MOE_OK
+
+
 def test_wait_limits_shorter_than_a_drain_are_refused(lib):
     """A CTA whose wait ran out waits as long again for its copies in flight: a limit of microseconds would let it
     leave before they land."""
