@@ -341,7 +341,8 @@ int moe_init(const moe_shape_t *shape, moe_ctx_t **out) {
         *slots[i] = sizes[i] ? b : nullptr;
         b += round256(sizes[i]);
     }
-    if (cudaMemset(c->ws, 0, total) != cudaSuccess) {
+    // (waited for: streams that do not block on the default one are not behind it)
+    if (cudaMemset(c->ws, 0, total) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
         cudaFree(c->ws);
         delete c;
         return MOE_ERR_CUDA;

@@ -589,3 +589,22 @@ def test_bounded_wait_reports_timeout_and_context_survives():
     res = compare_block(_y_numpy(y), idx.cpu().numpy(), wts.cpu().numpy(), ref, 4, 8)
     assert res["ok"], res
     m.close()
+
+
+def test_new_context_on_a_stream_of_its_own():
+    """The workspace of a new context is zero for a stream that is not ordered behind the default one, which is kept
+    busy here: the same bits as on the default stream."""
+    inp = custom_layer(T=16, d=128, F=128, E=8, k=4, seed=2)
+    x, w, s = _bf16_dev(inp["x"]), moe.MoEWeights.from_numpy(inp), torch.cuda.Stream()
+    m = moe.MoE(16, 128, 128, 8, 4)
+    want = m.forward(x, w)
+    torch.cuda.synchronize()
+    m.close()
+    for _ in range(10):
+        torch.cuda._sleep(2_000_000)
+        m = moe.MoE(16, 128, 128, 8, 4)
+        with torch.cuda.stream(s):
+            y = m.forward(x, w)
+            assert m.sync_status(s) == moe.MOE_OK
+        assert torch.equal(y, want)
+        m.close()
